@@ -250,6 +250,61 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
                                         void *alpha, void *workspace, size_t workspace_bytes,
                                         void *stream);
 
+/*
+ * Distillation loss against a teacher's top logits: what trains a compressed model to answer
+ * as the dense one that it came from.  Row n holds the student's logits x [V] and up to K of
+ * the teacher's logits t_j with their columns i_j:
+ *
+ *   p    = softmax_j(t_j / tau) over the row's entries,   q = softmax(x / tau)
+ *   loss[n] = w_n ( (1 - lam) tau^2 sum_j p_j (log p_j - log q_{i_j})
+ *                   + lam (log sum exp(x) - x_label) )
+ *   dlogits[n][v] = w_n dloss_n ( (1 - lam) tau (q_v - sum_{j: i_j = v} p_j)
+ *                                 + lam (softmax(x)_v - [v = label]) )
+ *
+ *   logits  [N] rows of V elements, `ld` elements apart (ld >= V); float32 (KRON_F32) or
+ *           bfloat16 (KRON_BF16); KRON_TF32 returns KRON_ERR_UNSUPPORTED
+ *   values  [N][K] float32; indices [N][K], index_bytes = 4 (int32) or 8 (int64).  An index
+ *           outside [0, V) is no entry, and its value is not looked at; neither has an entry
+ *           of value -inf any weight.  A column may be listed more than once: its
+ *           probabilities add up.  A row without entries has no teacher term.  1 <= K <= 1024.
+ *   labels  [N] int64; a label outside [0, V) (such as -100) is none: the row's second term
+ *           is zero.  May be NULL when lam = label_weight is 0.
+ *   weights [N] float32, NULL = ones.  A row of weight 0 gives loss 0 and gradient 0 whatever
+ *           its logits hold.
+ *   loss    [N] float32, not reduced
+ *   lse     [N][2] float32: the log-sum-exp of the row at the temperature and at one, which
+ *           kron_distill_backward takes (one that the gradient does not need repeats the
+ *           other); forward: may be NULL
+ *   dloss   [N] float32, the gradient of `loss`, NULL = ones
+ *   dlogits rows ld_out elements apart, of the logits' type; may be the logits themselves
+ *           (the same pointer and stride), and does not overlap them otherwise
+ *   1e-3 <= temperature <= 1e3, 0 <= label_weight <= 1
+ * kron_distill_step gives `loss` and the `dlogits` of the sum of `loss` in one call, reading
+ * the logits from memory once.  Sums are formed in float32 in a fixed order: results are bitwise
+ * reproducible.  No workspace.  Tensors need the alignment of their elements; rows that are
+ * also 16-byte aligned alike in logits and dlogits are stored 16 bytes at a time.  Everything
+ * else as for the layer above.
+ */
+KRON_API kron_status_t kron_distill_forward(const void *logits, int64_t ld, const float *values,
+                                            const void *indices, int index_bytes,
+                                            const int64_t *labels, const float *weights,
+                                            float *loss, float *lse, int64_t N, int64_t V, int K,
+                                            double temperature, double label_weight,
+                                            kron_dtype_t dtype, void *stream);
+KRON_API kron_status_t kron_distill_backward(const void *logits, int64_t ld, const float *values,
+                                             const void *indices, int index_bytes,
+                                             const int64_t *labels, const float *weights,
+                                             const float *lse, const float *dloss, void *dlogits,
+                                             int64_t ld_out, int64_t N, int64_t V, int K,
+                                             double temperature, double label_weight,
+                                             kron_dtype_t dtype, void *stream);
+KRON_API kron_status_t kron_distill_step(const void *logits, int64_t ld, const float *values,
+                                         const void *indices, int index_bytes,
+                                         const int64_t *labels, const float *weights, float *loss,
+                                         void *dlogits, int64_t ld_out, int64_t N, int64_t V,
+                                         int K, double temperature, double label_weight,
+                                         kron_dtype_t dtype, void *stream);
+
 /* Bytes of device workspace kron_linear_backward needs for this problem (0 if the
  * arguments are invalid).  Depends only on the arguments, not on the device. */
 KRON_API size_t kron_linear_workspace_size(int64_t N, int p, int q, int m1, int m2, int r,

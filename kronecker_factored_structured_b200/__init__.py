@@ -12,6 +12,10 @@ The same library holds the Kronecker-sparse factor of the page "Fast Inference
 with Kronecker-Sparse Matrices" (support kron(I_a, kron(1_{b x c}, I_d)),
 include/ks_linear.h): ``native.ks_forward`` / ``native.ks_backward``, wrapped by
 ``KSLinearFunction`` / ``KSLinear``.
+
+``distill_loss`` / ``DistillLoss`` train a compressed model on its dense original's top logits
+(``native.distill_forward`` / ``distill_backward``; ``native.distill_step`` gives the loss and
+its gradient from one call).
 """
 from __future__ import annotations
 
@@ -24,7 +28,7 @@ from .native import KronError, backward, forward, workspace_size
 
 __all__ = ["native", "accounting", "forward", "backward", "workspace_size", "KronError",
            "KronLinearFunction", "KronLinear", "kron_linear", "KSLinearFunction", "KSLinear",
-           "ks_linear"]
+           "ks_linear", "DistillFunction", "DistillLoss", "distill_loss"]
 
 
 class KronLinearFunction(torch.autograd.Function):
@@ -125,3 +129,63 @@ class KSLinear(torch.nn.Module):
         shp = x.shape
         y = ks_linear(x.reshape(-1, shp[-1]).contiguous(), self.w, self.bias)
         return y.reshape(*shp[:-1], y.shape[-1])
+
+
+class DistillFunction(torch.autograd.Function):
+    """Autograd wrapper of the distillation loss: a loss per row, the gradient in the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, values, indices, labels, weights, temperature, label_weight):
+        g = native.distill_forward(logits, values, indices, labels, weights, temperature,
+                                   label_weight)
+        ctx.save_for_backward(logits, values, indices, labels, weights, g["lse"])
+        ctx.temperature, ctx.label_weight = temperature, label_weight
+        return g["loss"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        logits, values, indices, labels, weights, lse = ctx.saved_tensors
+        d = native.distill_backward(logits, values, indices, lse, dloss.contiguous(), labels,
+                                    weights, ctx.temperature, ctx.label_weight)
+        return d, None, None, None, None, None, None
+
+
+def distill_loss(logits, values, indices, labels=None, weights=None, temperature=1.0,
+                 label_weight=0.0, reduction="mean"):
+    """(1 - label_weight) temperature^2 KL(teacher || student) over the teacher's top logits
+    plus label_weight times the cross-entropy with ``labels``, per row of ``logits``.
+
+    ``values`` (float32) and ``indices`` hold the teacher's logits of each row and their
+    columns, an index outside the vocabulary being no entry; shapes are (..., V), (..., K) and
+    (...).  ``weights`` multiplies the rows.  reduction: "none" (the rows' losses), "sum", or
+    "mean" (the sum over the sum of ``weights``, or over the rows without them).  The teacher
+    gets no gradient.
+    """
+    if reduction not in ("none", "sum", "mean"):
+        raise ValueError(f"reduction must be 'none', 'sum' or 'mean', got {reduction!r}")
+    lead = logits.shape[:-1]
+    flat = lambda t: None if t is None else t.reshape(-1).contiguous()  # noqa: E731
+    weights = flat(weights)
+    loss = DistillFunction.apply(
+        logits.reshape(-1, logits.shape[-1]), values.reshape(-1, values.shape[-1]).contiguous(),
+        indices.reshape(-1, indices.shape[-1]).contiguous(), flat(labels), weights,
+        float(temperature), float(label_weight))
+    if reduction == "none":
+        return loss.reshape(lead)
+    if reduction == "sum":
+        return loss.sum()
+    return loss.sum() / (loss.numel() if weights is None else weights.sum())
+
+
+class DistillLoss(torch.nn.Module):
+    """``distill_loss`` with its temperature, label weight and reduction kept."""
+
+    def __init__(self, temperature=1.0, label_weight=0.0, reduction="mean"):
+        super().__init__()
+        self.temperature, self.label_weight = float(temperature), float(label_weight)
+        self.reduction = reduction
+
+    def forward(self, logits, values, indices, labels=None, weights=None):
+        return distill_loss(logits, values, indices, labels, weights, self.temperature,
+                            self.label_weight, self.reduction)

@@ -1,0 +1,541 @@
+// distill.cu -- distillation loss against a teacher's top logits (kron_distill_forward,
+// kron_distill_backward, kron_distill_step; include/kron_linear.h).
+//
+// Row n of the student's logits x [V], the teacher's K logits t_j at the columns i_j:
+//   p_j  = softmax_j(t_j / tau) over the row's entries,   q = softmax(x / tau)
+//   loss = w [ (1 - lam) tau^2 sum_j p_j (log p_j - log q_{i_j}) + lam (lse(x) - x_label) ]
+//   dx_v = w dl [ (1 - lam) tau (q_v - sum_{j: i_j = v} p_j) + lam (softmax(x)_v - [v = label]) ]
+//
+// One CTA per row.  Pass 1 reads the row once with a running maximum m and the sums of
+// exp((x - m)/tau) and exp(x - m) per thread; pass 2 (gradient) reads it again, from L2, and
+// writes the dense part c_t q + c_1 softmax(x); the K + 1 columns that the teacher and the
+// label touch are then overwritten by the thread that owns the first entry of the column,
+// in fp32, from logits fetched before anything is written (so dlogits may be the logits).
+// Bound: HBM (one read, one write of the logits); per element one or two ex2.
+#include "../../include/kron_linear.h"
+#include "internal.h"
+
+#include <cuda_bf16.h>
+#include <math.h>
+#include <stdio.h>
+
+namespace kron {
+kron_status_t report_failure(kron_status_t st, const char *msg);
+
+namespace {
+
+constexpr int kMaxK = 1024;      // teacher entries per row
+constexpr int kThreads = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Args {
+    const void *logits;
+    int64_t ld;
+    const float *values;
+    const void *indices;
+    const int64_t *labels;
+    const float *weights;
+    const float *dloss;
+    float *loss;
+    float *lse;
+    const float *lse_in;
+    void *dlogits;
+    int64_t ld_out;
+    int V, K;
+    float tau, lam;
+    bool idx64;
+};
+
+// How the two exponentials of one logit are formed.
+enum Exps {
+    kOne,     // one temperature only (tau = 1, or one of the two terms has weight zero)
+    kSquare,  // tau = 2: exp(x) = exp(x/2)^2
+    kFourth,  // tau = 4
+    kTwo      // any other tau
+};
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+template <typename T> struct Vec;
+template <> struct Vec<float> {
+    static constexpr int n = 4;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4]) {
+        f[0] = __uint_as_float(u.x);
+        f[1] = __uint_as_float(u.y);
+        f[2] = __uint_as_float(u.z);
+        f[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                          __float_as_uint(f[3]));
+    }
+    static __device__ __forceinline__ float get(const float *p) { return *p; }
+    static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
+};
+template <> struct Vec<__nv_bfloat16> {
+    static constexpr int n = 8;
+    static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ float get(const __nv_bfloat16 *p) {
+        return __bfloat162float(*p);
+    }
+    static __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) {
+        *p = __float2bfloat16_rn(v);
+    }
+};
+
+// Running maximum of the logits and the sums of exp((x - m) a / log2 e) for the two scales.
+struct Stat {
+    float m, s, s1;
+};
+
+template <int E> __device__ __forceinline__ float second(float e, float d) {
+    if constexpr (E == kSquare) return e * e;
+    if constexpr (E == kFourth) return (e * e) * (e * e);
+    if constexpr (E == kTwo) return ex2(d * kLog2e);
+    return 0.f;
+}
+
+// Moves the sums of `st` to the maximum m (>= st.m).  A maximum of -inf means nothing but
+// -inf has been seen, and the sums are then zero.
+template <int E> __device__ __forceinline__ void rebase(Stat &st, float m, float a) {
+    if (m > st.m) {
+        const float d = st.m - m;      // -inf at the first finite value: factors 0
+        const float e = ex2(d * a);
+        st.s *= e;
+        if constexpr (E != kOne) st.s1 *= second<E>(e, d);
+        st.m = m;
+    }
+}
+
+template <int E> __device__ __forceinline__ void merge(Stat &st, const Stat &o, float a) {
+    Stat t = o;
+    const float m = fmaxf(st.m, t.m);
+    rebase<E>(st, m, a);
+    rebase<E>(t, m, a);
+    st.s += t.s;
+    if constexpr (E != kOne) st.s1 += t.s1;
+}
+
+template <int E> __device__ __forceinline__ void add_one(Stat &st, float x, float a) {
+    rebase<E>(st, x, a);
+    // -inf contributes nothing (also while every value so far is -inf); a NaN or +inf makes
+    // the sum NaN, as the definition does
+    const float d = x == -INFINITY ? -INFINITY : x - st.m;
+    const float e = ex2(d * a);
+    st.s += e;
+    if constexpr (E != kOne) st.s1 += second<E>(e, d);
+}
+
+template <int E> __device__ __forceinline__ Stat shuffle_xor(const Stat &st, int o) {
+    Stat t;
+    t.m = __shfl_xor_sync(0xffffffffu, st.m, o);
+    t.s = __shfl_xor_sync(0xffffffffu, st.s, o);
+    t.s1 = E == kOne ? 0.f : __shfl_xor_sync(0xffffffffu, st.s1, o);
+    return t;
+}
+
+// What a row needs of the teacher, in shared memory: columns (-1: no entry), probabilities,
+// student logits at the columns.
+struct RowSmem {
+    int col[kMaxK];
+    float prob[kMaxK];
+    float x[kMaxK];
+    Stat warp[32];
+    float red[32];
+    float redm[32];
+    Stat row;
+    float tsum;
+};
+
+// Sum over the CTA in a fixed order; every thread gets it.
+__device__ __forceinline__ float block_sum(float v, float *red) {
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.f;
+    for (int i = 0; i < kThreads / 32; ++i) t += red[i];
+    return t;
+}
+__device__ __forceinline__ float block_max(float v, float *red) {
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = -INFINITY;
+    for (int i = 0; i < kThreads / 32; ++i) t = fmaxf(t, red[i]);
+    return t;
+}
+
+template <typename T, int E, bool STATS, bool GRAD>
+__global__ void __launch_bounds__(kThreads) distill_kernel(const Args g) {
+    __shared__ RowSmem sm;
+    using Vc = Vec<T>;
+    constexpr int n = Vc::n;
+    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x;
+    const T *x = static_cast<const T *>(g.logits) + row * g.ld;
+    T *out = GRAD ? static_cast<T *>(g.dlogits) + row * g.ld_out : nullptr;
+    const float w = g.weights ? g.weights[row] : 1.f;
+    const float coef = GRAD ? (g.dloss ? w * g.dloss[row] : w) : w;
+    const int V = g.V, K = g.K;
+
+    // 16-byte body of the row, aligned for the logits; the gradient's vector stores also
+    // need the output row at the same offset from a 16-byte boundary
+    const int head = min(V, (int)(((16 - ((uintptr_t)x & 15)) & 15) / sizeof(T)));
+    const int nv = (V - head) / n;
+    const uint4 *xv = reinterpret_cast<const uint4 *>(x + head);
+    const bool same = GRAD && (((uintptr_t)x ^ (uintptr_t)out) & 15) == 0;
+
+    if (coef == 0.f) {   // a row without weight: zero, whatever its logits hold
+        if (STATS && tid == 0) {
+            g.loss[row] = 0.f;
+            if (g.lse) g.lse[2 * row] = g.lse[2 * row + 1] = 0.f;
+        }
+        if (GRAD)
+            for (int v = tid; v < V; v += kThreads) Vc::put(out + v, 0.f);
+        return;
+    }
+
+    // the temperature of the (only, or first) exponential
+    const bool hard_only = g.lam == 1.f;
+    const float inv_tau = hard_only ? 1.f : 1.f / g.tau;
+    const float a = kLog2e * inv_tau;
+
+    // ---- the teacher's distribution over the row's entries
+    float tm = -INFINITY;
+    for (int j = tid; j < K; j += kThreads) {
+        const int64_t i = g.idx64 ? static_cast<const int64_t *>(g.indices)[row * K + j]
+                                  : static_cast<const int *>(g.indices)[row * K + j];
+        const bool there = i >= 0 && i < V;
+        const float t = there ? g.values[row * K + j] : -INFINITY;
+        sm.col[j] = there ? (int)i : -1;
+        sm.prob[j] = t;
+        sm.x[j] = there ? Vc::get(x + i) : 0.f;
+        tm = fmaxf(tm, t);
+    }
+    const int64_t lab64 = g.labels ? g.labels[row] : -1;
+    const int label = lab64 >= 0 && lab64 < V ? (int)lab64 : -1;
+    const float xlab = label >= 0 ? Vc::get(x + label) : 0.f;
+    tm = block_max(tm, sm.redm);
+    float ts = 0.f;
+    for (int j = tid; j < K; j += kThreads) {
+        const float t = sm.prob[j];
+        const float e = t == -INFINITY ? 0.f : ex2((t - tm) * (kLog2e / g.tau));
+        sm.prob[j] = e;
+        ts += e;
+    }
+    ts = block_sum(ts, sm.red);
+    const bool any = ts != 0.f;   // NaN counts: it has to show
+    const float its = any ? 1.f / ts : 0.f;
+
+    // ---- the student's log-sum-exp at both temperatures
+    float lse_t, lse_1;
+    if constexpr (STATS) {
+        Stat st{-INFINITY, 0.f, 0.f};
+        for (int v = tid; v < nv; v += kThreads) {
+            float f[n];
+            Vc::unpack(xv[v], f);
+            float m = f[0];
+#pragma unroll
+            for (int i = 1; i < n; ++i) m = fmaxf(m, f[i]);
+            rebase<E>(st, m, a);
+            const float base = st.m == -INFINITY ? 0.f : st.m;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float d = f[i] - base;
+                const float e = ex2(d * a);
+                st.s += e;
+                if constexpr (E != kOne) st.s1 += second<E>(e, d);
+            }
+        }
+        if (tid < head) add_one<E>(st, Vc::get(x + tid), a);
+        const int tail = head + nv * n + tid;
+        if (tail < V) add_one<E>(st, Vc::get(x + tail), a);
+        for (int o = 16; o; o >>= 1) {
+            const Stat t = shuffle_xor<E>(st, o);
+            merge<E>(st, t, a);
+        }
+        if ((tid & 31) == 0) sm.warp[tid >> 5] = st;
+        __syncthreads();
+        Stat r = sm.warp[0];
+        for (int i = 1; i < kThreads / 32; ++i) merge<E>(r, sm.warp[i], a);
+        const float lsum = logf(r.s);
+        lse_t = r.m * inv_tau + lsum;
+        lse_1 = E == kOne ? lse_t : r.m + logf(r.s1);
+        // (with one exponential and both terms, tau is 1 and the two agree)
+
+        // ---- the loss
+        const float llse = logf(ts);
+        float kl = 0.f;
+        if (!hard_only)
+            for (int j = tid; j < K; j += kThreads) {
+                const float e = sm.prob[j];
+                if (sm.col[j] >= 0 && e != 0.f) {
+                    const float lp = (g.values[row * K + j] - tm) * inv_tau - llse;
+                    const float lq = (sm.x[j] - r.m) * inv_tau - lsum;
+                    kl += e * its * (lp - lq);
+                }
+            }
+        kl = block_sum(kl, sm.red);
+        if (tid == 0) {
+            float l = (1.f - g.lam) * g.tau * g.tau * kl;
+            if (g.lam != 0.f && label >= 0) l += g.lam * (lse_1 - xlab);
+            g.loss[row] = w * l;
+            if (g.lse) {
+                g.lse[2 * row] = lse_t;
+                g.lse[2 * row + 1] = lse_1;
+            }
+        }
+    } else {
+        lse_t = hard_only ? g.lse_in[2 * row + 1] : g.lse_in[2 * row];
+        lse_1 = g.lse_in[2 * row + 1];
+    }
+    if constexpr (!GRAD) return;
+
+    // ---- the gradient: c_t q + c_1 softmax(x), less the teacher's and the label's share
+    const float soft = hard_only || !any ? 0.f : coef * (1.f - g.lam) * g.tau;
+    const float hard = g.lam != 0.f && label >= 0 ? coef * g.lam : 0.f;
+    const float c_t = E == kOne ? soft + hard : soft;
+    const float b_t = -lse_t * kLog2e, b_1 = -lse_1 * kLog2e;
+    // exp(x - lse_1) from q: (q exp(lse_t - lse_1/tau))^tau, the factor in [1, V]
+    const float lift = E == kSquare ? ex2((lse_t - 0.5f * lse_1) * kLog2e)
+                                    : E == kFourth ? ex2((lse_t - 0.25f * lse_1) * kLog2e) : 1.f;
+    auto dense = [&](float v) {
+        const float e = ex2(fmaf(v, a, b_t));
+        float d = c_t == 0.f ? 0.f : c_t * e;
+        if constexpr (E == kSquare || E == kFourth) {
+            const float f = e * lift, f2 = f * f;
+            d = fmaf(hard, E == kSquare ? f2 : f2 * f2, d);
+        }
+        if constexpr (E == kTwo) d = fmaf(hard, ex2(fmaf(v, kLog2e, b_1)), d);
+        return d;
+    };
+    __syncthreads();   // every gather of the row is done before it may be overwritten
+    for (int v = tid; v < nv; v += kThreads) {
+        float f[n];
+        Vc::unpack(xv[v], f);
+#pragma unroll
+        for (int i = 0; i < n; ++i) f[i] = dense(f[i]);
+        T *o = out + head + v * n;
+        if (same) {
+            *reinterpret_cast<uint4 *>(o) = Vc::pack(f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; ++i) Vc::put(o + i, f[i]);
+        }
+    }
+    if (tid < head) Vc::put(out + tid, dense(Vc::get(x + tid)));
+    const int tail = head + nv * n + tid;
+    if (tail < V) Vc::put(out + tail, dense(Vc::get(x + tail)));
+    __syncthreads();
+    for (int j = tid; j < K; j += kThreads) {
+        const int c = sm.col[j];
+        if (c < 0) continue;
+        float p = 0.f;
+        bool first = true;      // a column listed more than once: its first entry writes it
+        for (int k = 0; k < K; ++k)
+            if (sm.col[k] == c) {
+                if (k < j) first = false;
+                p += sm.prob[k];
+            }
+        const float teacher = soft == 0.f ? 0.f : soft * its * p;
+        if (first) Vc::put(out + c, dense(sm.x[j]) - teacher - (c == label ? hard : 0.f));
+    }
+    if (tid == 0 && label >= 0) {
+        bool listed = false;
+        for (int k = 0; k < K; ++k) listed = listed || sm.col[k] == label;
+        if (!listed) Vc::put(out + label, dense(xlab) - hard);
+    }
+}
+
+kron_status_t bad(kron_status_t st, const char *fmt, double a = 0, double b = 0) {
+    char msg[224];
+    snprintf(msg, sizeof(msg), fmt, a, b);
+    return report_failure(st, msg);
+}
+
+template <typename T, bool STATS, bool GRAD>
+cudaError_t launch_exps(int exps, unsigned grid, const Args &g, cudaStream_t st) {
+    switch (exps) {
+        case kOne: distill_kernel<T, kOne, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
+        case kSquare: distill_kernel<T, kSquare, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
+        case kFourth: distill_kernel<T, kFourth, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
+        default: distill_kernel<T, kTwo, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
+    }
+    return cudaGetLastError();
+}
+
+template <bool STATS, bool GRAD>
+kron_status_t run(const Args &g, int64_t N, kron_dtype_t dtype, void *stream) {
+    const bool one = g.tau == 1.f || g.lam == 0.f || g.lam == 1.f;
+    const int exps = one ? kOne : g.tau == 2.f ? kSquare : g.tau == 4.f ? kFourth : kTwo;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e =
+        dtype == KRON_BF16
+            ? launch_exps<__nv_bfloat16, STATS, GRAD>(exps, (unsigned)N, g, st)
+            : launch_exps<float, STATS, GRAD>(exps, (unsigned)N, g, st);
+    if (e != cudaSuccess) {
+        char msg[200];
+        snprintf(msg, sizeof(msg), "distillation launch: %s", cudaGetErrorString(e));
+        return report_failure(KRON_ERR_CUDA, msg);
+    }
+    return KRON_OK;
+}
+
+// The checks that every entry point shares.
+kron_status_t check(const void *logits, int64_t ld, const void *values, const void *indices,
+                    int index_bytes, const void *labels, const void *weights, int64_t N, int64_t V,
+                    int K, double tau, double lam, kron_dtype_t dtype) {
+    report_failure(KRON_OK, "");
+    if (dtype != KRON_F32 && dtype != KRON_BF16)
+        return bad(KRON_ERR_UNSUPPORTED, "the loss takes KRON_F32 or KRON_BF16 logits (dtype %g)",
+                   (double)dtype);
+    if (N < 0 || N > 0x7fffffff || V < 1 || V > (1 << 30) || K < 1)
+        return bad(KRON_ERR_INVALID_ARG,
+                   "sizes must be 0 <= N < 2^31, 1 <= V <= 2^30, K >= 1 (N = %g, V = %g)",
+                   (double)N, (double)V);
+    if (K > kMaxK)
+        return bad(KRON_ERR_UNSUPPORTED, "at most %g teacher logits per row (K = %g)",
+                   (double)kMaxK, (double)K);
+    if (ld < V) return bad(KRON_ERR_INVALID_ARG, "row stride %g below V = %g", (double)ld, (double)V);
+    if (index_bytes != 4 && index_bytes != 8)
+        return bad(KRON_ERR_INVALID_ARG, "indices have 4 or 8 bytes (got %g)", index_bytes);
+    if (!(tau >= 1e-3 && tau <= 1e3))
+        return bad(KRON_ERR_INVALID_ARG, "the temperature must be in [1e-3, 1e3] (got %g)", tau);
+    if (!(lam >= 0.0 && lam <= 1.0))
+        return bad(KRON_ERR_INVALID_ARG, "the label weight must be in [0, 1] (got %g)", lam);
+    if (lam > 0.0 && !labels && N > 0)
+        return bad(KRON_ERR_INVALID_ARG, "labels are needed when their weight is above 0 (%g)", lam);
+    if (N > 0 && (!logits || !values || !indices))
+        return bad(KRON_ERR_INVALID_ARG, "logits, values and indices must be non-null");
+    const uintptr_t e = dtype == KRON_BF16 ? 1 : 3;
+    if (((uintptr_t)logits & e) || ((uintptr_t)values & 3) ||
+        ((uintptr_t)indices & (uintptr_t)(index_bytes - 1)) || ((uintptr_t)labels & 7) ||
+        ((uintptr_t)weights & 3))
+        return bad(KRON_ERR_ALIGNMENT, "tensors must be aligned to their element size");
+    return KRON_OK;
+}
+
+Args args(const void *logits, int64_t ld, const float *values, const void *indices,
+          int index_bytes, const int64_t *labels, const float *weights, int64_t V, int K,
+          double tau, double lam) {
+    Args g{};
+    g.logits = logits;
+    g.ld = ld;
+    g.values = values;
+    g.indices = indices;
+    g.labels = lam > 0.0 ? labels : nullptr;
+    g.weights = weights;
+    g.V = (int)V;
+    g.K = K;
+    g.tau = (float)tau;
+    g.lam = (float)lam;
+    g.idx64 = index_bytes == 8;
+    return g;
+}
+
+}  // namespace
+}  // namespace kron
+
+using namespace kron;
+
+extern "C" {
+
+kron_status_t kron_distill_forward(const void *logits, int64_t ld, const float *values,
+                                   const void *indices, int index_bytes, const int64_t *labels,
+                                   const float *weights, float *loss, float *lse, int64_t N,
+                                   int64_t V, int K, double temperature, double label_weight,
+                                   kron_dtype_t dtype, void *stream) {
+    const kron_status_t st = check(logits, ld, values, indices, index_bytes, labels, weights, N, V,
+                                   K, temperature, label_weight, dtype);
+    if (st != KRON_OK) return st;
+    if (N > 0 && !loss) return bad(KRON_ERR_INVALID_ARG, "loss must be non-null");
+    if (((uintptr_t)loss | (uintptr_t)lse) & 3)
+        return bad(KRON_ERR_ALIGNMENT, "loss and lse must be 4-byte aligned");
+    if (N == 0) return KRON_OK;
+    Args g = args(logits, ld, values, indices, index_bytes, labels, weights, V, K, temperature,
+                  label_weight);
+    g.loss = loss;
+    g.lse = lse;
+    return run<true, false>(g, N, dtype, stream);
+}
+
+kron_status_t kron_distill_backward(const void *logits, int64_t ld, const float *values,
+                                    const void *indices, int index_bytes, const int64_t *labels,
+                                    const float *weights, const float *lse, const float *dloss,
+                                    void *dlogits, int64_t ld_out, int64_t N, int64_t V, int K,
+                                    double temperature, double label_weight, kron_dtype_t dtype,
+                                    void *stream) {
+    const kron_status_t st = check(logits, ld, values, indices, index_bytes, labels, weights, N, V,
+                                   K, temperature, label_weight, dtype);
+    if (st != KRON_OK) return st;
+    if (N > 0 && (!lse || !dlogits))
+        return bad(KRON_ERR_INVALID_ARG, "lse and dlogits must be non-null");
+    if (logits && dlogits == logits && ld_out != ld)
+        return bad(KRON_ERR_INVALID_ARG, "in place, both row strides are the same (%g, %g)",
+                   (double)ld, (double)ld_out);
+    if (ld_out < V)
+        return bad(KRON_ERR_INVALID_ARG, "row stride %g of dlogits below V = %g", (double)ld_out,
+                   (double)V);
+    if ((((uintptr_t)lse | (uintptr_t)dloss) & 3) ||
+        ((uintptr_t)dlogits & (dtype == KRON_BF16 ? 1 : 3)))
+        return bad(KRON_ERR_ALIGNMENT, "tensors must be aligned to their element size");
+    if (N == 0) return KRON_OK;
+    Args g = args(logits, ld, values, indices, index_bytes, labels, weights, V, K, temperature,
+                  label_weight);
+    g.lse_in = lse;
+    g.dloss = dloss;
+    g.dlogits = dlogits;
+    g.ld_out = ld_out;
+    return run<false, true>(g, N, dtype, stream);
+}
+
+kron_status_t kron_distill_step(const void *logits, int64_t ld, const float *values,
+                                const void *indices, int index_bytes, const int64_t *labels,
+                                const float *weights, float *loss, void *dlogits, int64_t ld_out,
+                                int64_t N, int64_t V, int K, double temperature,
+                                double label_weight, kron_dtype_t dtype, void *stream) {
+    const kron_status_t st = check(logits, ld, values, indices, index_bytes, labels, weights, N, V,
+                                   K, temperature, label_weight, dtype);
+    if (st != KRON_OK) return st;
+    if (N > 0 && (!loss || !dlogits))
+        return bad(KRON_ERR_INVALID_ARG, "loss and dlogits must be non-null");
+    if (logits && dlogits == logits && ld_out != ld)
+        return bad(KRON_ERR_INVALID_ARG, "in place, both row strides are the same (%g, %g)",
+                   (double)ld, (double)ld_out);
+    if (ld_out < V)
+        return bad(KRON_ERR_INVALID_ARG, "row stride %g of dlogits below V = %g", (double)ld_out,
+                   (double)V);
+    if (((uintptr_t)loss & 3) || ((uintptr_t)dlogits & (dtype == KRON_BF16 ? 1 : 3)))
+        return bad(KRON_ERR_ALIGNMENT, "tensors must be aligned to their element size");
+    if (N == 0) return KRON_OK;
+    Args g = args(logits, ld, values, indices, index_bytes, labels, weights, V, K, temperature,
+                  label_weight);
+    g.loss = loss;
+    g.dlogits = dlogits;
+    g.ld_out = ld_out;
+    return run<true, true>(g, N, dtype, stream);
+}
+
+}  // extern "C"

@@ -32,6 +32,7 @@ EXPORTS = ("kron_linear_forward", "kron_linear_backward", "kron_linear_backward_
            "kron_linear_backward_noalloc",
            "kron_linear_workspace_size", "kron_vanloan_fit", "kron_vanloan_workspace_size",
            "kron3_linear_forward", "kron3_linear_backward", "kron3_linear_workspace_size",
+           "kron_distill_forward", "kron_distill_backward", "kron_distill_step",
            "kron_status_string", "kron_last_error", "kron_linear_device_error",
            "kron_linear_abi_version",
            "ks_linear_forward", "ks_linear_backward", "ks_linear_workspace_size")
@@ -81,6 +82,16 @@ def load(path: str = LIB_PATH):
     lib.kron3_linear_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, I, I, I,
                                           I, I, I, I, I, U, vp, sz, vp]
     lib.kron3_linear_backward.restype = I
+    D = ctypes.c_double
+    lib.kron_distill_forward.argtypes = [vp, i64, vp, vp, I, vp, vp, vp, vp, i64, i64, I, D, D, I,
+                                         vp]
+    lib.kron_distill_forward.restype = I
+    lib.kron_distill_backward.argtypes = [vp, i64, vp, vp, I, vp, vp, vp, vp, vp, i64, i64, i64, I,
+                                          D, D, I, vp]
+    lib.kron_distill_backward.restype = I
+    lib.kron_distill_step.argtypes = [vp, i64, vp, vp, I, vp, vp, vp, vp, i64, i64, i64, I, D, D,
+                                      I, vp]
+    lib.kron_distill_step.restype = I
     lib.kron_linear_workspace_size.argtypes = [i64, I, I, I, I, I, I]
     lib.kron_linear_workspace_size.restype = sz
     lib.kron_status_string.argtypes = [I]
@@ -347,3 +358,105 @@ def ks_backward(x, w, dY, need_dx=True, need_dbias=True, workspace=None, grads=N
                                      _ptr(g["dbias"]), N, a, b, c, d, KRON_F32, 0,
                                      _ptr(workspace), workspace.numel(), _stream(stream)))
     return g
+
+
+# ---- distillation loss against a teacher's top logits ----
+
+def _on(dev, name, t):
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _rows(t, name, dtype, N, V):
+    """A matrix whose rows are contiguous and may lie further apart than their length."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (N, V):
+        raise ValueError(f"{name} must have shape {(N, V)}, got {tuple(t.shape)}")
+    if not t.is_cuda or (V > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < V):
+        raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
+    return t.stride(0) if N > 1 else V
+
+
+def _distill_args(logits, values, indices, labels, weights, label_weight):
+    if logits.dim() != 2 or values.dim() != 2:
+        raise ValueError("logits must have shape (N, V), values and indices (N, K)")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    N, V = logits.shape
+    K = values.shape[1]
+    ld = _rows(logits, "logits", logits.dtype, N, V)
+    _expect(values, "values", torch.float32, (N, K))
+    if indices.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"indices must be int32 or int64, got {indices.dtype}")
+    _expect(indices, "indices", indices.dtype, (N, K))
+    if label_weight and labels is None:
+        raise ValueError("labels are needed when label_weight is above 0")
+    if labels is not None:
+        _expect(labels, "labels", torch.int64, (N,))
+    if weights is not None:
+        _expect(weights, "weights", torch.float32, (N,))
+    for name, t in (("values", values), ("indices", indices), ("labels", labels),
+                    ("weights", weights)):
+        if t is not None:
+            _on(logits.device, name, t)
+    head = (_ptr(logits), ld, _ptr(values), _ptr(indices), indices.element_size(), _ptr(labels),
+            _ptr(weights))
+    dtype = KRON_BF16 if logits.dtype == torch.bfloat16 else KRON_F32
+    return N, V, K, head, dtype
+
+
+def _dlogits(logits, out):
+    N, V = logits.shape
+    if out is None:
+        out = torch.empty(N, V, dtype=logits.dtype, device=logits.device)
+    ld = _rows(out, "dlogits", logits.dtype, N, V)
+    _on(logits.device, "dlogits", out)
+    return out, ld
+
+
+def distill_forward(logits, values, indices, labels=None, weights=None, temperature=1.0,
+                    label_weight=0.0, stream=None):
+    """Loss of each row against the teacher's top logits: dict(loss [N], lse [N][2])."""
+    N, V, K, head, dtype = _distill_args(logits, values, indices, labels, weights, label_weight)
+    dev = logits.device
+    with torch.cuda.device(dev):
+        loss = torch.empty(N, dtype=torch.float32, device=dev)
+        lse = torch.empty(N, 2, dtype=torch.float32, device=dev)
+        _check(load().kron_distill_forward(*head, _ptr(loss), _ptr(lse), N, V, K,
+                                           float(temperature), float(label_weight), dtype,
+                                           _stream(stream)))
+    return {"loss": loss, "lse": lse}
+
+
+def distill_backward(logits, values, indices, lse, dloss=None, labels=None, weights=None,
+                     temperature=1.0, label_weight=0.0, out=None, stream=None):
+    """Gradient of <dloss, loss> in the logits (``dloss`` None: ones).  ``out`` may be the
+    logits themselves, which the gradient then overwrites."""
+    N, V, K, head, dtype = _distill_args(logits, values, indices, labels, weights, label_weight)
+    dev = logits.device
+    for name, t, shp in (("lse", lse, (N, 2)), ("dloss", dloss, (N,))):
+        if t is not None:
+            _expect(t, name, torch.float32, shp)
+            _on(dev, name, t)
+    with torch.cuda.device(dev):
+        out, ld_out = _dlogits(logits, out)
+        _check(load().kron_distill_backward(*head, _ptr(lse), _ptr(dloss), _ptr(out), ld_out, N, V,
+                                            K, float(temperature), float(label_weight), dtype,
+                                            _stream(stream)))
+    return out
+
+
+def distill_step(logits, values, indices, labels=None, weights=None, temperature=1.0,
+                 label_weight=0.0, out=None, stream=None):
+    """Loss of each row and the gradient of their sum, the logits read once:
+    dict(loss [N], dlogits).  ``out`` may be the logits themselves."""
+    N, V, K, head, dtype = _distill_args(logits, values, indices, labels, weights, label_weight)
+    dev = logits.device
+    with torch.cuda.device(dev):
+        loss = torch.empty(N, dtype=torch.float32, device=dev)
+        out, ld_out = _dlogits(logits, out)
+        _check(load().kron_distill_step(*head, _ptr(loss), _ptr(out), ld_out, N, V, K,
+                                        float(temperature), float(label_weight), dtype,
+                                        _stream(stream)))
+    return {"loss": loss, "dlogits": out}
