@@ -251,6 +251,51 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
                                         void *stream);
 
 /*
+ * The gated half of a feed-forward block over two projections of this layer's form:
+ *
+ *     h = act(x Wg + bg) * (x Wu + bu),   W* = sum_i kron(S* (.) A*_i, B*_i)
+ *
+ * The projections are stacked, gate first:
+ *   S, dS [2][p][q];  A, dA [2][r][p][q];  B, dB [2][r][m1][m2];  bias, dbias [2][q*m2]
+ *   x, dX [N][p*m1];  h, dH [N][q*m2]
+ * `activation` is a kron_activation_t.  flags must be 0.
+ *   KRON_F32   every tensor float32, exact FP32 arithmetic (the layer's CUDA-core kernels)
+ *   KRON_BF16  every tensor bfloat16, the gradients too (each rounded once from float32);
+ *              tcgen05 tensor cores: both projections, the activation and the product in one
+ *              kernel.  Sizes are run-time values; m1 and m2 multiples of 8, p and q at most
+ *              1024, and the factors of some slice of the layer have to fit shared memory, else
+ *              KRON_ERR_UNSUPPORTED (about r p <= 1000 and r m1 <= 2000)
+ *   KRON_TF32  KRON_ERR_UNSUPPORTED
+ * Backward: gradients of <dH, h>; the pre-activations are formed again, nothing is kept from
+ * the forward call.  bias may be NULL (none); dX and dbias may be NULL (skipped).  On KRON_BF16
+ * T = X B and the pre-activations' gradients are rounded to bfloat16 between the products.
+ * With N == 0 the forward is a no-op and the factor gradients are zero.
+ * `workspace`: kron_glu_workspace_size(..., backward) bytes (forward: 0; may be 0 bytes, and
+ * workspace then NULL), 256-byte aligned, owned by the caller; two calls that may run at the
+ * same time need one each.  0 also means arguments that the call refuses.  N <= 2^30.
+ * Results are bitwise reproducible on one GPU model.  Everything else as for the layer.
+ */
+typedef enum {
+    KRON_ACT_SILU = 0,      /* g sigmoid(g)                                        */
+    KRON_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2                         */
+    KRON_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2     */
+    KRON_ACT_SIGMOID = 3    /* sigmoid(g)                                          */
+} kron_activation_t;
+KRON_API size_t kron_glu_workspace_size(int64_t N, int p, int q, int m1, int m2, int r,
+                                        kron_dtype_t dtype, int backward);
+KRON_API kron_status_t kron_glu_forward(const void *x, const void *S, const void *A, const void *B,
+                                        const void *bias, void *h, int64_t N, int p, int q,
+                                        int m1, int m2, int r, int activation, kron_dtype_t dtype,
+                                        unsigned flags, void *workspace, size_t workspace_bytes,
+                                        void *stream);
+KRON_API kron_status_t kron_glu_backward(const void *x, const void *S, const void *A,
+                                         const void *B, const void *bias, const void *dH, void *dX,
+                                         void *dS, void *dA, void *dB, void *dbias, int64_t N,
+                                         int p, int q, int m1, int m2, int r, int activation,
+                                         kron_dtype_t dtype, unsigned flags, void *workspace,
+                                         size_t workspace_bytes, void *stream);
+
+/*
  * Distillation loss against a teacher's top logits: what trains a compressed model to answer
  * as the dense one that it came from.  Row n holds the student's logits x [V] and up to K of
  * the teacher's logits t_j with their columns i_j:

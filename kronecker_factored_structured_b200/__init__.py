@@ -13,6 +13,9 @@ with Kronecker-Sparse Matrices" (support kron(I_a, kron(1_{b x c}, I_d)),
 include/ks_linear.h): ``native.ks_forward`` / ``native.ks_backward``, wrapped by
 ``KSLinearFunction`` / ``KSLinear``.
 
+``KronGLU`` is the gated half of a feed-forward block, act(x Wg + bg) * (x Wu + bu), over two
+projections of the layer's form; ``KronGatedFFN`` puts a ``KronLinear`` behind it.
+
 ``distill_loss`` / ``DistillLoss`` train a compressed model on its dense original's top logits
 (``native.distill_forward`` / ``distill_backward``; ``native.distill_step`` gives the loss and
 its gradient from one call).
@@ -28,7 +31,7 @@ from .native import KronError, backward, forward, workspace_size
 
 __all__ = ["native", "accounting", "forward", "backward", "workspace_size", "KronError",
            "KronLinearFunction", "KronLinear", "kron_linear", "KSLinearFunction", "KSLinear",
-           "ks_linear", "DistillFunction", "DistillLoss", "distill_loss"]
+           "ks_linear", "KronGLUFunction", "KronGLU", "kron_glu", "KronGatedFFN", "DistillFunction", "DistillLoss", "distill_loss"]
 
 
 class KronLinearFunction(torch.autograd.Function):
@@ -129,6 +132,79 @@ class KSLinear(torch.nn.Module):
         shp = x.shape
         y = ks_linear(x.reshape(-1, shp[-1]).contiguous(), self.w, self.bias)
         return y.reshape(*shp[:-1], y.shape[-1])
+
+
+class KronGLUFunction(torch.autograd.Function):
+    """Autograd wrapper of the gated half; both passes run in the CUDA library, and the
+    backward forms the pre-activations again from the saved inputs."""
+
+    @staticmethod
+    def forward(ctx, x, S, A, B, bias, activation, dtype):
+        ctx.save_for_backward(x, S, A, B, bias)
+        ctx.activation, ctx.dtype = activation, dtype
+        return native.glu_forward(x, S, A, B, bias, activation, dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dH):
+        x, S, A, B, bias = ctx.saved_tensors
+        g = native.glu_backward(x, S, A, B, dH.contiguous(), bias, ctx.activation, ctx.dtype,
+                                need_dx=ctx.needs_input_grad[0], need_dbias=bias is not None)
+        return g["dX"], g["dS"], g["dA"], g["dB"], g["dbias"], None, None
+
+
+def kron_glu(x, S, A, B, bias=None, activation="silu", dtype="bf16"):
+    """act(x Wg + bg) * (x Wu + bu) with W* = sum_i kron(S* (.) A*_i, B*_i): S (2, p, q),
+    A (2, r, p, q), B (2, r, m1, m2) and bias (2, q*m2) hold the gate, then the up projection."""
+    return KronGLUFunction.apply(x, S, A, B, bias, activation, dtype)
+
+
+class KronGLU(torch.nn.Module):
+    """Gated half of a feed-forward block: two Kronecker-factored projections, an activation
+    ("silu", "gelu", "gelu_tanh", "sigmoid") and the product.  Factors are initialised as
+    ``KronLinear``'s.  dtype "bf16" (tensor cores) or "f32" (exact)."""
+
+    def __init__(self, in_features, hidden_features, block_in, block_out=None, rank=1, bias=True,
+                 activation="silu", dtype="bf16", device=None):
+        super().__init__()
+        block_out = block_in if block_out is None else block_out
+        if in_features % block_in or hidden_features % block_out:
+            raise ValueError("features must be multiples of the block size")
+        if dtype not in ("f32", "bf16"):
+            raise ValueError(f"the gated half runs on 'f32' and 'bf16', got {dtype!r}")
+        if activation not in native.ACTIVATIONS:
+            raise ValueError(f"activation must be one of {sorted(native.ACTIVATIONS)}, "
+                             f"got {activation!r}")
+        p, q = in_features // block_in, hidden_features // block_out
+        kw = dict(device=device, dtype=native.io_dtype(dtype))
+        self.S = torch.nn.Parameter(torch.ones(2, p, q, **kw))
+        self.A = torch.nn.Parameter(torch.randn(2, rank, p, q, **kw) / math.sqrt(p))
+        self.B = torch.nn.Parameter(torch.randn(2, rank, block_in, block_out, **kw)
+                                    / math.sqrt(block_in))
+        self.bias = (torch.nn.Parameter(torch.zeros(2, hidden_features, **kw)) if bias else None)
+        self.activation, self.path = activation, dtype
+
+    def forward(self, x):
+        h = kron_glu(x.reshape(-1, x.shape[-1]).contiguous(), self.S, self.A, self.B, self.bias,
+                     self.activation, self.path)
+        return h.reshape(*x.shape[:-1], h.shape[-1])
+
+
+class KronGatedFFN(torch.nn.Module):
+    """Gated feed-forward block of Kronecker-factored projections: ``KronGLU`` (``glu``) to the
+    hidden width, ``KronLinear`` (``down``) back, whose shapes and dtypes are its own."""
+
+    def __init__(self, features, hidden_features, block, hidden_block=None, rank=1, bias=True,
+                 activation="silu", dtype="bf16", device=None):
+        super().__init__()
+        hidden_block = block if hidden_block is None else hidden_block
+        self.glu = KronGLU(features, hidden_features, block, hidden_block, rank, bias, activation,
+                           dtype, device)
+        self.down = KronLinear(hidden_features, features, hidden_block, block, rank, bias, dtype,
+                               device=device)
+
+    def forward(self, x):
+        return self.down(self.glu(x))
 
 
 class DistillFunction(torch.autograd.Function):

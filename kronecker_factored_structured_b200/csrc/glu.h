@@ -1,0 +1,101 @@
+// glu.h -- declarations shared by the translation units of the gated Kronecker feed-forward
+// half (glu.cu, glu_tc.cu, glu_wgrad.cu): h = act(x Wg + bg) * (x Wu + bu).
+#pragma once
+
+#include "../../include/kron_linear.h"
+#include "internal.h"
+
+namespace kron {
+namespace glu {
+
+// What one run of the two-stage tensor-core kernel computes.
+enum Mode {
+    kForward,  // h from x
+    kPre,      // dg = dH u act'(g) and du = dH act(g), both pre-activations formed again
+    kInput     // dX = dg Wg^T + du Wu^T
+};
+
+// The kernel's tiles for one shape and mode.  In its own terms the kernel contracts P groups
+// of M1 values into Q groups of M2 values (kInput: the layer's q, m2, p, m1).
+struct Plan {
+    int P, M1, Q, M2, r;
+    int nsrc, ranks;          // sources, and ranks that contract each of them
+    int MP, NT, RB;           // k columns per slice, rows per tile, ranks per block: NT = RB
+    int rbl;                  // ranks of the fullest block
+    int nac, AC;              // chunks of the a index, and their width
+    int nblk, nblk_src;       // rank blocks in all and per source
+    int sw, kch, kb;          // x rows: swizzle width, chunks of it per row, bytes per row
+    int nacc;                 // accumulators (gate and up, or their sum)
+    int nqs, qc, qcp, nks;    // c slices, columns per slice (and padded to 16), k slices
+    int ybufs, stages;
+    int off_c, off_t, off_x, smem;   // shared memory: B^T at 0, C', T, x ring
+    int t_bytes, x_bytes, c_chunk;
+    int ntiles, groups;       // row tiles, and CTAs per slice
+};
+
+bool tc_plan(Plan *pl, const Shape &s, Mode mode, int sms);
+
+struct TcArgs {
+    const void *src0, *src1;      // x, or dg and du
+    const void *S, *A, *B, *bias; // stacked gate and up
+    const void *dH;
+    void *out0, *out1;            // h or dX; dg and du
+    int64_t N;
+    int activation;
+};
+cudaError_t tc_run(const Plan &pl, const TcArgs &a, Mode mode, cudaStream_t st);
+
+// Dense weight gradients of the two projections, x^T [dg | du], in split row ranges, then
+// the factors' gradients from them.
+struct WgradPlan {
+    int splits;
+    int64_t rows_per_split;
+    size_t part_floats;       // one split: [2][din][dout] and the column sums [2][dout]
+    int dbs;                  // ranges of (a) that dB's partial sums are split into
+    size_t ws_bytes;
+};
+WgradPlan wgrad_plan(const Shape &s, int sms);
+cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const void *du,
+                      const void *S, const void *A, const void *B, void *dS, void *dA, void *dB,
+                      void *dbias, void *ws, const Shape &s, cudaStream_t st);
+
+// Activation and derivative from hardware exponentials and reciprocals (about 2^-21 of the
+// value: far below the bfloat16 rounding of what is stored).
+__device__ __forceinline__ float sigmoid_fast(float g) {
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    return __fdividef(1.f, 1.f + e);
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_fast(float g, float *d) {
+    if constexpr (ACT == KRON_ACT_SILU) {
+        const float s = sigmoid_fast(g), f = g * s;
+        if (d) *d = s + f * (1.f - s);
+        return f;
+    } else if constexpr (ACT == KRON_ACT_SIGMOID) {
+        const float s = sigmoid_fast(g);
+        if (d) *d = s * (1.f - s);
+        return s;
+    } else if constexpr (ACT == KRON_ACT_GELU) {
+        const float c = 0.5f + 0.5f * erff(g * 0.70710678f);
+        if (d) {
+            float e;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752f));
+            *d = c + (e == 0.f ? 0.f : g * e * 0.39894228f);
+        }
+        return g * c;
+    } else {
+        // (1 + tanh(v)) / 2 = sigmoid(2 v) with v = sqrt(2/pi) (g + 0.044715 g^3)
+        const float g2 = g * g;
+        const float s = sigmoid_fast(1.5957691f * g * (1.f + 0.044715f * g2));
+        if (d) {
+            const float w = s * (1.f - s);
+            *d = s + (w == 0.f ? 0.f : g * w * 1.5957691f * (1.f + 0.134145f * g2));
+        }
+        return g * s;
+    }
+}
+
+}  // namespace glu
+}  // namespace kron

@@ -1,0 +1,412 @@
+// glu_wgrad.cu -- factor gradients of the gated Kronecker feed-forward half, BF16.
+//
+// With dW = x^T d (d = dg or du), block (a, c) of dW the m1 x m2 matrix dW[a,.,c,.]:
+//   dC_i[a,c] = sum_(j,k) B_i[j,k] dW[a,j,c,k]     dA_i = dC_i (.) S, dS = sum_i dC_i (.) A_i
+//   dB_i[j,k] = sum_(a,c) C_i[a,c] dW[a,j,c,k]     dbias = column sums of d
+// dW is formed densely by one tcgen05 product over the rows (both operands as they lie in
+// memory, MN-major), then contracted with the factors in fp32.  For the vec trick's own order
+// (T = X B against d, C d against X) the row sums take r (1/q + 1/m1) of dW's multiply-adds,
+// twice, but T and C d of every row have to go through registers and shared memory, which is
+// what bounds those kernels; dW is a plain product that runs at the tensor cores' rate.
+// Rows are split into ranges whose dW are added in order: bitwise reproducible.
+#include "glu.h"
+#include "tc_gen_common.cuh"
+
+#include <cuda_bf16.h>
+
+namespace kron {
+namespace glu {
+
+using namespace tc;
+using namespace tc::gen;
+
+namespace {
+
+// ---- dW = x^T [dg | du]: tiles of 128 x 256, K = 64 rows per stage ----
+constexpr int kTM = 128, kTN = 256, kTK = 64, kStages = 4;
+constexpr int kABytes = kTM * kTK * 2, kBBytes = kTN * kTK * 2, kStageBytes = kABytes + kBBytes;
+constexpr int kBoxBytes = 64 * kTK * 2;        // one TMA box: 64 columns x 64 rows
+constexpr int kDwThreads = 192;                // TMA, MMA, four column-sum / epilogue warps
+constexpr size_t kDwSmem = (size_t)kStages * kStageBytes + 1024 + 256;
+
+struct DwArgs {
+    float *part;
+    size_t part_floats;
+    int64_t N, rows_per_split;
+    int din, dout, mt, nt;       // tiles along din, and along dout of one projection
+    int sums;                    // whether the column sums are wanted
+    int *device_error;
+};
+
+enum { kFull = 0, kEmpty = kStages, kDone = 2 * kStages, kDwBars = 2 * kStages + 1 };
+
+__global__ void __launch_bounds__(kDwThreads, 1)
+glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mg,
+              const __grid_constant__ CUtensorMap mu, const DwArgs g) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+    const uint32_t tail = base + kStages * kStageBytes;
+    uint8_t *tail_ptr = smem_raw + (tail - raw);
+    auto bar = [&](int i) { return tail + 8u * i; };
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail_ptr + kDwBars * 8);
+    const Abort ab{reinterpret_cast<volatile int *>(tail_ptr + kDwBars * 8 + 8), g.device_error};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    const int tiles = g.mt * g.nt * 2;
+    const int split = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+    const int m0 = (tile % g.mt) * kTM, proj = tile / (g.mt * g.nt);
+    const int n0 = (tile / g.mt) % g.nt * kTN;
+    const int64_t r0 = split * g.rows_per_split;
+    const int64_t r1 = min(g.N, r0 + g.rows_per_split);
+    const int steps = (int)((r1 - r0 + kTK - 1) / kTK);
+    const bool sums = g.sums && m0 == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar(kFull + s), 1);
+            mbar_init(bar(kEmpty + s), sums ? 5 : 1);
+        }
+        mbar_init(bar(kDone), 1);
+        *ab.flag = 0;
+        mbar_init_fence();
+        prefetch_tmap(&mx);
+        prefetch_tmap(proj ? &mu : &mg);
+    }
+    if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    bool done = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int u = 0;
+            for (; u < steps; ++u) {
+                const int s = u % kStages;
+                if (!mbar_wait(bar(kEmpty + s), ((u / kStages) & 1) ^ 1, ab)) break;
+                const uint32_t a = base + s * kStageBytes, b = a + kABytes;
+                const int row = (int)(r0 + (int64_t)u * kTK);
+                mbar_arrive_expect_tx(bar(kFull + s), kStageBytes);
+                for (int i = 0; i < kTM / 64; ++i)
+                    tma_load_2d(a + i * kBoxBytes, &mx, m0 + i * 64, row, bar(kFull + s));
+                for (int i = 0; i < kTN / 64; ++i)
+                    tma_load_2d(b + i * kBoxBytes, proj ? &mu : &mg, n0 + i * 64, row,
+                                bar(kFull + s));
+            }
+            for (int v = u > kStages ? u - kStages : 0; v < u; ++v)
+                mbar_wait_drain(bar(kFull + v % kStages), (v / kStages) & 1);
+        }
+    } else if (warp == 1) {
+        // both operands MN-major (bits 15 and 16): K runs down the rows of a box
+        constexpr uint32_t idesc = idesc_f32acc(kTM, kTN, 1) | (1u << 15) | kBMajorMN;
+        for (int u = 0; u < steps; ++u) {
+            const int s = u % kStages;
+            if (!warp_wait(bar(kFull + s), (u / kStages) & 1, ab)) break;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t a = base + s * kStageBytes;
+                const uint64_t ad = sdesc_mn(a, layout_type(128), kBoxBytes, 1024);
+                const uint64_t bd = sdesc_mn(a + kABytes, layout_type(128), kBoxBytes, 1024);
+#pragma unroll
+                for (int kk = 0; kk < kTK / 16; ++kk)
+                    mma_ss<false>(tmem, desc_add(ad, kk * 2048), desc_add(bd, kk * 2048), idesc,
+                                  (u > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(bar(kEmpty + s));
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(bar(kDone));
+        __syncwarp();
+        if (lane == 0) mbar_wait_drain(bar(kDone), 0);
+        __syncwarp();
+    } else {
+        const int quad = warp & 3, t = (warp - 2) * 32 + lane;
+        float *part = g.part + (size_t)split * g.part_floats;
+        if (sums) {
+            // columns 2t and 2t + 1 of the d tile, rows in order
+            float s0 = 0.f, s1 = 0.f;
+            const int col = 2 * t, box = col / 64, inb = (col % 64) * 2;
+            bool ok = true;
+            for (int u = 0; u < steps; ++u) {
+                const int s = u % kStages;
+                if (!warp_wait(bar(kFull + s), (u / kStages) & 1, ab)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t b = base + s * kStageBytes + kABytes + box * kBoxBytes;
+#pragma unroll 16
+                for (int r = 0; r < kTK; ++r) {
+                    uint32_t w;
+                    asm volatile("ld.shared.b32 %0, [%1];"
+                                 : "=r"(w)
+                                 : "r"(b + swz((uint32_t)(r * 128 + inb), 128))
+                                 : "memory");
+                    s0 += __uint_as_float(w << 16);
+                    s1 += __uint_as_float(w & 0xFFFF0000u);
+                }
+                mbar_arrive_warp(bar(kEmpty + s));
+            }
+            if (ok) {
+                float *dst = part + (size_t)2 * g.din * g.dout + (size_t)proj * g.dout + n0 + col;
+                if (n0 + col < g.dout) dst[0] = s0;
+                if (n0 + col + 1 < g.dout) dst[1] = s1;
+            }
+        }
+        done = warp_wait(bar(kDone), 0, ab);
+        tc_fence_after();
+        if (done) {
+            const int row = m0 + quad * 32 + lane;
+            float *dst = part + ((size_t)proj * g.din + row) * g.dout + n0;
+            for (int cg = 0; cg < kTN / 32; ++cg) {
+                if (n0 + cg * 32 >= g.dout) break;
+                uint32_t v[32];
+                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + cg * 32, v);
+                if (row < g.din) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (n0 + cg * 32 + i < g.dout)
+                            *reinterpret_cast<uint4 *>(dst + cg * 32 + i) =
+                                make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 256);
+}
+
+// ---- contraction with the factors ----
+constexpr int kCt = 256;      // threads
+constexpr int kRc = 8;        // ranks summed at a time
+constexpr int kCc = 4;        // columns c per warp (dC)
+
+struct CtArgs {
+    const float *part;
+    size_t part_floats;
+    int splits;
+    const __nv_bfloat16 *S, *A, *B;
+    __nv_bfloat16 *dS, *dA;
+    float *dbp;                  // [dbs][2][r][m1][m2]
+    int p, q, m1, m2, r, dout, dbs;
+    int dc_blocks;               // blocks of the first role
+};
+
+__device__ __forceinline__ float dw_sum(const CtArgs &g, size_t o) {
+    float v = __ldg(g.part + o);
+    for (int s = 1; s < g.splits; ++s) v += __ldg(g.part + (size_t)s * g.part_floats + o);
+    return v;
+}
+
+// dC, dA, dS: a warp per (projection, a, four columns c)
+__device__ void dc_role(const CtArgs &g) {
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * (kCt / 32) + (threadIdx.x >> 5);
+    const int ncg = cdiv(g.q, kCc);
+    if (w >= (int64_t)2 * g.p * ncg) return;
+    const int c0 = (int)(w % ncg) * kCc, a = (int)(w / ncg % g.p), proj = (int)(w / ncg / g.p);
+    const size_t row0 = ((size_t)proj * g.p + a) * g.m1;   // rows of dW: (proj, a, j)
+    float ds[kCc] = {};
+    for (int i0 = 0; i0 < g.r; i0 += kRc) {
+        float acc[kCc][kRc] = {};
+        const __nv_bfloat16 *Bi = g.B + ((size_t)proj * g.r + i0) * g.m1 * g.m2;
+        const int ni = min(kRc, g.r - i0);
+        for (int e = lane; e < g.m1 * g.m2; e += 32) {
+            const int j = e / g.m2, k = e - j * g.m2;
+            const size_t o = (row0 + j) * g.dout + (size_t)c0 * g.m2 + k;
+            float v[kCc];
+#pragma unroll
+            for (int t = 0; t < kCc; ++t)
+                v[t] = c0 + t < g.q ? dw_sum(g, o + (size_t)t * g.m2) : 0.f;
+#pragma unroll
+            for (int i = 0; i < kRc; ++i) {
+                const float b =
+                    i < ni ? __bfloat162float(Bi[(size_t)i * g.m1 * g.m2 + e]) : 0.f;
+#pragma unroll
+                for (int t = 0; t < kCc; ++t) acc[t][i] = fmaf(v[t], b, acc[t][i]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < kCc; ++t)
+#pragma unroll
+            for (int i = 0; i < kRc; ++i)
+                for (int o = 16; o; o >>= 1)
+                    acc[t][i] += __shfl_xor_sync(0xffffffffu, acc[t][i], o);
+        if (lane == 0) {
+            for (int t = 0; t < kCc && c0 + t < g.q; ++t) {
+                const size_t pos = (size_t)a * g.q + c0 + t, pq = (size_t)g.p * g.q;
+                const float s = __bfloat162float(g.S[proj * pq + pos]);
+#pragma unroll
+                for (int i = 0; i < kRc; ++i)
+                    if (i < ni) {
+                        const size_t ai = ((size_t)proj * g.r + i0 + i) * pq + pos;
+                        g.dA[ai] = __float2bfloat16_rn(acc[t][i] * s);
+                        ds[t] = fmaf(acc[t][i], __bfloat162float(g.A[ai]), ds[t]);
+                    }
+            }
+        }
+    }
+    if (lane == 0)
+        for (int t = 0; t < kCc && c0 + t < g.q; ++t)
+            g.dS[(size_t)proj * g.p * g.q + (size_t)a * g.q + c0 + t] = __float2bfloat16_rn(ds[t]);
+}
+
+// dB partial sums: a thread per (j, k), a block per (projection, range of a, ranks)
+__device__ void db_role(const CtArgs &g, int blk) {
+    extern __shared__ float cs[];      // C_i[a][.] of one a: [kRc][q]
+    const int eb = cdiv(g.m1 * g.m2, kCt), ib = cdiv(g.r, kRc);
+    const int e = (blk % eb) * kCt + threadIdx.x;
+    blk /= eb;
+    const int i0 = (blk % ib) * kRc;
+    blk /= ib;
+    const int range = blk % g.dbs, proj = blk / g.dbs;
+    const int ni = min(kRc, g.r - i0);
+    const int a0 = (int)((int64_t)g.p * range / g.dbs), a1 = (int)((int64_t)g.p * (range + 1) / g.dbs);
+    const bool live = e < g.m1 * g.m2;
+    const int j = live ? e / g.m2 : 0, k = live ? e - j * g.m2 : 0;
+    float acc[kRc] = {};
+    const size_t pq = (size_t)g.p * g.q;
+    for (int a = a0; a < a1; ++a) {
+        __syncthreads();
+        for (int u = threadIdx.x; u < kRc * g.q; u += kCt) {
+            const int i = u / g.q, c = u - i * g.q;
+            const size_t pos = (size_t)a * g.q + c;
+            cs[u] = i < ni ? __bfloat162float(g.S[proj * pq + pos]) *
+                                 __bfloat162float(g.A[((size_t)proj * g.r + i0 + i) * pq + pos])
+                           : 0.f;
+        }
+        __syncthreads();
+        if (live) {
+            const size_t o = (((size_t)proj * g.p + a) * g.m1 + j) * g.dout + k;
+#pragma unroll 4
+            for (int c = 0; c < g.q; ++c) {
+                const float v = dw_sum(g, o + (size_t)c * g.m2);
+#pragma unroll
+                for (int i = 0; i < kRc; ++i) acc[i] = fmaf(v, cs[i * g.q + c], acc[i]);
+            }
+        }
+    }
+    if (live)
+#pragma unroll
+        for (int i = 0; i < kRc; ++i)
+            if (i < ni)
+                g.dbp[((((size_t)range * 2 + proj) * g.r + i0 + i) * g.m1 * g.m2) + e] = acc[i];
+}
+
+__global__ void __launch_bounds__(kCt) glu_contract_kernel(const CtArgs g) {
+    if ((int)blockIdx.x < g.dc_blocks) dc_role(g);
+    else db_role(g, blockIdx.x - g.dc_blocks);
+}
+
+// dB and dbias: the ranges and splits added in order.
+__global__ void __launch_bounds__(kCt)
+glu_finish_kernel(const float *dbp, int dbs, size_t nb, __nv_bfloat16 *dB, const float *sums,
+                  size_t part_floats, int splits, size_t nbias, __nv_bfloat16 *dbias) {
+    const size_t e = (size_t)blockIdx.x * kCt + threadIdx.x;
+    if (e < nb) {
+        float v = 0.f;
+        for (int s = 0; s < dbs; ++s) v += dbp[(size_t)s * nb + e];
+        dB[e] = __float2bfloat16_rn(v);
+    } else if (dbias && e - nb < nbias) {
+        float v = 0.f;
+        for (int s = 0; s < splits; ++s) v += sums[(size_t)s * part_floats + e - nb];
+        dbias[e - nb] = __float2bfloat16_rn(v);
+    }
+}
+
+size_t pad64(size_t n) { return (n + 63) & ~(size_t)63; }
+
+}  // namespace
+
+WgradPlan wgrad_plan(const Shape &s, int sms) {
+    WgradPlan pl{};
+    const int din = (int)s.d_in(), dout = (int)s.d_out();
+    const int64_t tiles = (int64_t)cdiv(din, kTM) * 2 * cdiv(dout, kTN);
+    int64_t splits = sms / tiles;
+    const int64_t most = (s.N + 255) / 256;    // at least four stages of rows per range
+    if (splits > most) splits = most;
+    if (splits < 1) splits = 1;
+    pl.rows_per_split = ((s.N + splits - 1) / splits + kTK - 1) / kTK * kTK;
+    if (pl.rows_per_split < kTK) pl.rows_per_split = kTK;
+    pl.splits = (int)((s.N + pl.rows_per_split - 1) / pl.rows_per_split);
+    if (pl.splits < 1) pl.splits = 1;
+    pl.part_floats = pad64((size_t)2 * din * dout + 2 * (size_t)dout);
+    // dB: enough ranges of a to fill the SMs about four times
+    const int64_t per = (int64_t)cdiv(s.m1 * s.m2, kCt) * cdiv(s.r, kRc) * 2;
+    int64_t dbs = (4 * sms + per - 1) / per;
+    if (dbs > s.p) dbs = s.p;
+    pl.dbs = (int)dbs;
+    pl.ws_bytes = 4 * (pl.part_floats * pl.splits +
+                       pad64((size_t)pl.dbs * 2 * s.r * s.m1 * s.m2));
+    return pl;
+}
+
+cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const void *du,
+                      const void *S, const void *A, const void *B, void *dS, void *dA, void *dB,
+                      void *dbias, void *ws, const Shape &s, cudaStream_t st) {
+    const int din = (int)s.d_in(), dout = (int)s.d_out();
+    CUtensorMap mx, mg, mu;
+    launch_step() = "tensor map";
+    cudaError_t e = make_tmap_2d(&mx, x, true, s.N, din, 64, kTK, 128, false);
+    if (e == cudaSuccess) e = make_tmap_2d(&mg, dg, true, s.N, dout, 64, kTK, 128, false);
+    if (e == cudaSuccess) e = make_tmap_2d(&mu, du, true, s.N, dout, 64, kTK, 128, false);
+    if (e != cudaSuccess) return e;
+    DwArgs g{};
+    g.part = static_cast<float *>(ws);
+    g.part_floats = pl.part_floats;
+    g.N = s.N;
+    g.rows_per_split = pl.rows_per_split;
+    g.din = din;
+    g.dout = dout;
+    g.mt = cdiv(din, kTM);
+    g.nt = cdiv(dout, kTN);
+    g.sums = dbias != nullptr;
+    launch_step() = "device error word";
+    g.device_error = device_error_ptr();
+    if (!g.device_error) return cudaErrorInvalidSymbol;
+    launch_step() = "shared memory size";
+    e = cudaFuncSetAttribute(glu_dw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kDwSmem);
+    if (e != cudaSuccess) return e;
+    launch_step() = "weight-gradient launch";
+    const int64_t grid = (int64_t)g.mt * g.nt * 2 * pl.splits;
+    glu_dw_kernel<<<(unsigned)grid, kDwThreads, kDwSmem, st>>>(mx, mg, mu, g);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    CtArgs c{};
+    c.part = g.part;
+    c.part_floats = pl.part_floats;
+    c.splits = pl.splits;
+    c.S = static_cast<const __nv_bfloat16 *>(S);
+    c.A = static_cast<const __nv_bfloat16 *>(A);
+    c.B = static_cast<const __nv_bfloat16 *>(B);
+    c.dS = static_cast<__nv_bfloat16 *>(dS);
+    c.dA = static_cast<__nv_bfloat16 *>(dA);
+    c.dbp = g.part + pl.part_floats * pl.splits;
+    c.p = s.p;
+    c.q = s.q;
+    c.m1 = s.m1;
+    c.m2 = s.m2;
+    c.r = s.r;
+    c.dout = dout;
+    c.dbs = pl.dbs;
+    c.dc_blocks = (int)(((int64_t)2 * s.p * cdiv(s.q, kCc) + kCt / 32 - 1) / (kCt / 32));
+    const int db_blocks = cdiv(s.m1 * s.m2, kCt) * cdiv(s.r, kRc) * pl.dbs * 2;
+    launch_step() = "factor-gradient launch";
+    glu_contract_kernel<<<(unsigned)(c.dc_blocks + db_blocks), kCt, (size_t)kRc * s.q * 4, st>>>(c);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const size_t nb = (size_t)2 * s.r * s.m1 * s.m2, nbias = dbias ? (size_t)2 * dout : 0;
+    launch_step() = "final sums launch";
+    glu_finish_kernel<<<(unsigned)((nb + nbias + kCt - 1) / kCt), kCt, 0, st>>>(
+        c.dbp, pl.dbs, nb, static_cast<__nv_bfloat16 *>(dB),
+        g.part + (size_t)2 * din * dout, pl.part_floats, pl.splits, nbias,
+        static_cast<__nv_bfloat16 *>(dbias));
+    return cudaGetLastError();
+}
+
+}  // namespace glu
+}  // namespace kron

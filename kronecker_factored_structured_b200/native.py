@@ -32,6 +32,7 @@ EXPORTS = ("kron_linear_forward", "kron_linear_backward", "kron_linear_backward_
            "kron_linear_backward_noalloc",
            "kron_linear_workspace_size", "kron_vanloan_fit", "kron_vanloan_workspace_size",
            "kron3_linear_forward", "kron3_linear_backward", "kron3_linear_workspace_size",
+           "kron_glu_forward", "kron_glu_backward", "kron_glu_workspace_size",
            "kron_distill_forward", "kron_distill_backward", "kron_distill_step",
            "kron_status_string", "kron_last_error", "kron_linear_device_error",
            "kron_linear_abi_version",
@@ -83,6 +84,12 @@ def load(path: str = LIB_PATH):
                                           I, I, I, I, I, U, vp, sz, vp]
     lib.kron3_linear_backward.restype = I
     D = ctypes.c_double
+    lib.kron_glu_workspace_size.argtypes = [i64, I, I, I, I, I, I, I]
+    lib.kron_glu_workspace_size.restype = sz
+    lib.kron_glu_forward.argtypes = [vp] * 6 + [i64] + [I] * 7 + [U, vp, sz, vp]
+    lib.kron_glu_forward.restype = I
+    lib.kron_glu_backward.argtypes = [vp] * 11 + [i64] + [I] * 7 + [U, vp, sz, vp]
+    lib.kron_glu_backward.restype = I
     lib.kron_distill_forward.argtypes = [vp, i64, vp, vp, I, vp, vp, vp, vp, i64, i64, I, D, D, I,
                                          vp]
     lib.kron_distill_forward.restype = I
@@ -360,11 +367,108 @@ def ks_backward(x, w, dY, need_dx=True, need_dbias=True, workspace=None, grads=N
     return g
 
 
-# ---- distillation loss against a teacher's top logits ----
-
 def _on(dev, name, t):
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+# ---- gated half of a feed-forward block: h = act(x Wg + bg) * (x Wu + bu) ----
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "sigmoid": 3}
+
+
+def glu_shapes(S, A, B):
+    """(p, q, m1, m2, r) of factors stacked [gate, up]."""
+    if S.dim() != 3 or A.dim() != 4 or B.dim() != 4:
+        raise ValueError("S must have shape (2, p, q), A (2, r, p, q) and B (2, r, m1, m2)")
+    two, r, p, q = A.shape
+    m1, m2 = B.shape[2:]
+    if two != 2 or tuple(S.shape) != (2, p, q) or tuple(B.shape[:2]) != (2, r):
+        raise ValueError(f"inconsistent factor shapes S{tuple(S.shape)} A{tuple(A.shape)} "
+                         f"B{tuple(B.shape)}")
+    return p, q, m1, m2, r
+
+
+def _glu_args(x, S, A, B, bias, activation, dtype):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    p, q, m1, m2, r = glu_shapes(S, A, B)
+    if x.dim() != 2:
+        raise ValueError(f"x must have shape (N, {p * m1}), got {tuple(x.shape)}")
+    N = x.shape[0]
+    t = io_dtype(dtype)
+    _expect(x, "x", t, (N, p * m1))
+    for name, v, shp in (("S", S, (2, p, q)), ("A", A, (2, r, p, q)), ("B", B, (2, r, m1, m2)),
+                         ("bias", bias, (2, q * m2))):
+        if v is not None:
+            _expect(v, name, t, shp)
+            _on(x.device, name, v)
+    return (N, p, q, m1, m2, r), t
+
+
+def glu_workspace_size(N, p, q, m1, m2, r, dtype="bf16", backward=False) -> int:
+    return int(load().kron_glu_workspace_size(N, p, q, m1, m2, r, DTYPES[dtype],
+                                              1 if backward else 0))
+
+
+def _glu_workspace(sizes, dtype, backward, workspace, dev):
+    n = glu_workspace_size(*sizes, dtype, backward)
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    _on(dev, "workspace", workspace)
+    return workspace
+
+
+def glu_forward(x, S, A, B, bias=None, activation="silu", dtype="bf16", out=None, workspace=None,
+                stream=None):
+    """h = act(x Wg + bg) * (x Wu + bu), W* = sum_i kron(S* (.) A*_i, B*_i); S [2][p][q],
+    A [2][r][p][q], B [2][r][m1][m2] and bias [2][q*m2] hold the gate, then the up projection.
+    dtype "f32" or "bf16"."""
+    sizes, t = _glu_args(x, S, A, B, bias, activation, dtype)
+    N, p, q, m1, m2, r = sizes
+    with torch.cuda.device(x.device):
+        if out is None:
+            out = torch.empty(N, q * m2, dtype=t, device=x.device)
+        _expect(out, "h", t, (N, q * m2))
+        _on(x.device, "h", out)
+        ws = _glu_workspace(sizes, dtype, False, workspace, x.device)
+        _check(load().kron_glu_forward(_ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(out),
+                                       *sizes, ACTIVATIONS[activation], DTYPES[dtype], 0, _ptr(ws),
+                                       0 if ws is None else ws.numel(), _stream(stream)))
+    return out
+
+
+def glu_backward(x, S, A, B, dH, bias=None, activation="silu", dtype="bf16", need_dx=True,
+                 need_dbias=True, workspace=None, grads=None, stream=None):
+    """Gradients of <dH, h>: dict(dX, dS, dA, dB, dbias) in the tensors' own dtype (None where
+    not asked).  ``grads`` may hold preallocated outputs."""
+    sizes, t = _glu_args(x, S, A, B, bias, activation, dtype)
+    N, p, q, m1, m2, r = sizes
+    dev = x.device
+    _expect(dH, "dH", t, (N, q * m2))
+    _on(dev, "dH", dH)
+    g = dict(grads or {})
+    with torch.cuda.device(dev):
+        for k, shp, need in (("dX", (N, p * m1), need_dx), ("dS", (2, p, q), True),
+                             ("dA", (2, r, p, q), True), ("dB", (2, r, m1, m2), True),
+                             ("dbias", (2, q * m2), need_dbias)):
+            if not need:
+                g[k] = None
+                continue
+            if g.get(k) is None:
+                g[k] = torch.empty(shp, dtype=t, device=dev)
+            _expect(g[k], k, t, shp)
+            _on(dev, k, g[k])
+        ws = _glu_workspace(sizes, dtype, True, workspace, dev)
+        _check(load().kron_glu_backward(_ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(dH),
+                                        _ptr(g["dX"]), _ptr(g["dS"]), _ptr(g["dA"]),
+                                        _ptr(g["dB"]), _ptr(g["dbias"]), *sizes,
+                                        ACTIVATIONS[activation], DTYPES[dtype], 0, _ptr(ws),
+                                        0 if ws is None else ws.numel(), _stream(stream)))
+    return g
+
+
+# ---- distillation loss against a teacher's top logits ----
 
 
 def _rows(t, name, dtype, N, V):

@@ -1,0 +1,98 @@
+"""Refusals of the gated half: every call below fails a host-side check, so nothing is launched
+and no GPU is needed."""
+import ctypes
+
+import pytest
+import torch
+
+import kronecker_factored_structured_b200 as kfs
+from kronecker_factored_structured_b200 import native
+
+V = ctypes.c_void_p
+OK, ODD = V(0x10000), V(0x10008)
+
+
+def call(backward, x=OK, S=OK, A=OK, B=OK, bias=OK, h=OK, dX=OK, dS=OK, dA=OK, dB=OK, dbias=OK,
+         N=8, p=4, q=4, m1=16, m2=16, r=2, act=0, dtype=2, flags=0, ws=OK, ws_bytes=1 << 40):
+    lib = native.load()
+    tail = (N, p, q, m1, m2, r, act, dtype, flags, ws, ws_bytes, None)
+    if backward:
+        return lib.kron_glu_backward(x, S, A, B, bias, h, dX, dS, dA, dB, dbias, *tail)
+    return lib.kron_glu_forward(x, S, A, B, bias, h, *tail)
+
+
+COMMON = [(dict(dtype=3), 1), (dict(dtype=1), 2), (dict(act=-1), 1), (dict(act=4), 1),
+          (dict(flags=1), 1), (dict(N=-1), 1), (dict(N=(1 << 30) + 1), 1), (dict(p=0), 1),
+          (dict(q=0), 1), (dict(r=0), 1), (dict(m1=0), 1), (dict(m1=12), 2), (dict(m2=4), 2),
+          (dict(m1=6, dtype=0), 2), (dict(p=1 << 20), 1), (dict(r=2000), 1), (dict(p=1025), 2),
+          (dict(p=64, q=64, m1=64, m2=64, r=100), 2),
+          (dict(p=4096, q=4096, m1=256, m2=256, r=64, dtype=0), 2),
+          (dict(x=None), 1), (dict(S=None), 1), (dict(A=None), 1), (dict(B=None), 1),
+          (dict(h=None), 1), (dict(x=ODD), 3), (dict(bias=ODD), 3), (dict(h=ODD), 3),
+          (dict(S=None, N=0), 1)]
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("kwargs,status", COMMON)
+def test_rejects(backward, kwargs, status):
+    assert call(backward, **kwargs) == status
+    assert native.load().kron_last_error().decode() != ""
+
+
+@pytest.mark.parametrize("kwargs,status", [
+    (dict(dS=None), 1), (dict(dA=None), 1), (dict(dB=None), 1), (dict(dX=ODD), 3),
+    (dict(dbias=ODD), 3), (dict(ws=None), 4), (dict(ws_bytes=100), 4), (dict(ws=V(0x10010)), 3)])
+@pytest.mark.parametrize("dtype", [0, 2])
+def test_backward_rejects(dtype, kwargs, status):
+    assert call(True, dtype=dtype, **kwargs) == status
+
+
+def test_forward_f32_wants_its_workspace():
+    assert call(False, dtype=0, ws=None) == 4
+    assert call(False, dtype=0, ws=V(0x10010)) == 3
+
+
+def test_empty_forward_is_fine():
+    assert call(False, N=0, x=None, h=None, ws=None, ws_bytes=0) == 0
+
+
+def test_workspace_size():
+    size = native.glu_workspace_size
+    assert size(100, 4, 4, 16, 16, 2, "bf16") == 0            # the forward needs none
+    assert size(100, 4, 4, 16, 16, 2, "f32") == 100 * 64 * 4
+    for dt in ("f32", "bf16"):
+        n = size(100, 4, 4, 16, 16, 2, dt, True)
+        assert n > 0 and n == size(100, 4, 4, 16, 16, 2, dt, True)
+    assert size(100, 4, 4, 16, 16, 2, "tf32", True) == 0
+    assert size(0, 4, 4, 16, 16, 2, "bf16", True) == 0
+
+
+def test_every_shape_of_a_wide_range_has_a_kernel():
+    """BF16: up to 64 groups of up to 64 values and eight terms, every multiple of eight."""
+    for p in (1, 8, 23, 64):
+        for q in (1, 9, 40, 64):
+            for m1 in (8, 24, 64):
+                for m2 in (8, 40, 64):
+                    for r in (1, 3, 8):
+                        assert native.glu_workspace_size(10, p, q, m1, m2, r, "bf16", True) > 0
+
+
+def test_binding_rejects():
+    S, A, B = torch.ones(2, 3, 4), torch.ones(2, 1, 3, 4), torch.ones(2, 1, 8, 8)
+    x = torch.ones(5, 24)
+    with pytest.raises(ValueError):
+        native.glu_forward(x, S, A, B, dtype="f32")                     # not on a GPU
+    with pytest.raises(TypeError):
+        native.glu_forward(x, S, A, B, dtype="bf16")
+    with pytest.raises(ValueError):
+        native.glu_forward(x, S, A, B, activation="relu", dtype="f32")
+    with pytest.raises(ValueError):
+        native.glu_forward(x, S[0], A, B, dtype="f32")
+    with pytest.raises(ValueError):
+        native.glu_forward(x, S, A[:, :, :2], B, dtype="f32")
+    with pytest.raises(ValueError):
+        kfs.KronGLU(96, 96, 32, dtype="tf32")
+    with pytest.raises(ValueError):
+        kfs.KronGLU(96, 96, 32, activation="relu")
+    with pytest.raises(ValueError):
+        kfs.KronGLU(96, 100, 32)
