@@ -262,8 +262,8 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
  *   KRON_F32   every tensor float32, exact FP32 arithmetic (the layer's CUDA-core kernels)
  *   KRON_BF16  every tensor bfloat16, the gradients too (each rounded once from float32);
  *              tcgen05 tensor cores: both projections, the activation and the product in one
- *              kernel.  Sizes are run-time values; m1 and m2 multiples of 8, p and q at most
- *              1024, and the factors of some slice of the layer have to fit shared memory, else
+ *              kernel.  Sizes are run-time values; m1 and m2 multiples of 8 up to 256, p and q
+ *              at most 1024, and the factors of some slice of the layer have to fit shared memory, else
  *              KRON_ERR_UNSUPPORTED (about r p <= 1000 and r m1 <= 2000)
  *   KRON_TF32  KRON_ERR_UNSUPPORTED
  * Backward: gradients of <dH, h>; the pre-activations are formed again, nothing is kept from

@@ -139,11 +139,11 @@ kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int ac
     const Shape s{N > 0 ? N : 1, p, q, m1, m2, r};
     Plan pl;
     if (dtype == KRON_BF16) {
-        if (p > 1024 || q > 1024 || !glu::tc_plan(&pl, s, glu::kForward, kRowParts) ||
+        if (p > 1024 || q > 1024 || m1 > 256 || m2 > 256 || !glu::tc_plan(&pl, s, glu::kForward, kRowParts) ||
             !glu::tc_plan(&pl, s, glu::kInput, kRowParts))
             return bad(KRON_ERR_UNSUPPORTED,
-                       "no tensor-core kernel for p=%d q=%d m1=%d m2=%d r=%d: the factors do not "
-                       "fit shared memory (KRON_F32 runs any shape)", p, q, m1, m2, r);
+                       "no tensor-core kernel for p=%d q=%d m1=%d m2=%d r=%d: blocks above 256 or "
+                       "factors that do not fit shared memory (KRON_F32 runs any shape)", p, q, m1, m2, r);
     } else if (simt_forward_rows(s) <= 0 || simt_backward_rows(s) <= 0) {
         return bad(KRON_ERR_UNSUPPORTED,
                    "no kernel for p=%d q=%d m1=%d m2=%d r=%d: the FP32 tile does not fit shared "

@@ -27,8 +27,11 @@ struct Plan {
     int sw, kch, kb;          // x rows: swizzle width, chunks of it per row, bytes per row
     int nacc;                 // accumulators (gate and up, or their sum)
     int nqs, qc, qcp, nks;    // c slices, columns per slice (and padded to 16), k slices
-    int ybufs, stages;
-    int off_c, off_t, off_x, smem;   // shared memory: B^T at 0, C', T, x ring
+    int ybufs, stages, tbufs, dbufs;   // buffers of Y, x, T and D1
+    int g1;                            // groups of epilogue-1 warps at work
+    int bias_smem, exact;              // biases in shared memory; no padding anywhere
+    int tm_y;                          // first TMEM column of Y
+    int off_c, off_t, off_x, off_bias, smem;   // shared memory: B^T at 0, C', T, x ring, biases
     int t_bytes, x_bytes, c_chunk;
     int ntiles, groups;       // row tiles, and CTAs per slice
 };
@@ -64,7 +67,9 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
 __device__ __forceinline__ float sigmoid_fast(float g) {
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    return __fdividef(1.f, 1.f + e);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));   // e = inf: 0
+    return r;
 }
 
 template <int ACT>

@@ -22,11 +22,14 @@ using namespace tc::gen;
 
 namespace {
 
-// ---- dW = x^T [dg | du]: tiles of 128 x 256, K = 64 rows per stage ----
-constexpr int kTM = 128, kTN = 256, kTK = 64, kStages = 4;
+// ---- dW = x^T [dg | du]: tiles of 256 x 256 (two M = 128 accumulators, all of TMEM), K = 64
+// rows per stage.  A stage brings 64 KB for 1024 cycles of MMA; with 128 x 256 tiles it was
+// 48 KB for 512, and the reads from L2 (96 B per cycle and SM) took twice the MMAs' time.
+constexpr int kTM = 256, kTN = 256, kTK = 64, kStages = 3;
 constexpr int kABytes = kTM * kTK * 2, kBBytes = kTN * kTK * 2, kStageBytes = kABytes + kBBytes;
 constexpr int kBoxBytes = 64 * kTK * 2;        // one TMA box: 64 columns x 64 rows
-constexpr int kDwThreads = 192;                // TMA, MMA, four column-sum / epilogue warps
+constexpr int kDwThreads = 320;                // TMA, MMA, eight epilogue warps (four also sum
+                                               // the columns of d)
 constexpr size_t kDwSmem = (size_t)kStages * kStageBytes + 1024 + 256;
 
 struct DwArgs {
@@ -60,6 +63,8 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     const int64_t r1 = min(g.N, r0 + g.rows_per_split);
     const int steps = (int)((r1 - r0 + kTK - 1) / kTK);
     const bool sums = g.sums && m0 == 0;
+    const bool second = m0 + 128 < g.din;      // whether the tile's lower half has rows of dW
+    const int a_boxes = second ? 4 : 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -72,7 +77,7 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         prefetch_tmap(&mx);
         prefetch_tmap(proj ? &mu : &mg);
     }
-    if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), 256);
+    if (warp == 1) tmem_alloc(smem_u32(const_cast<uint32_t *>(tmem_slot)), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -87,8 +92,8 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
                 if (!mbar_wait(bar(kEmpty + s), ((u / kStages) & 1) ^ 1, ab)) break;
                 const uint32_t a = base + s * kStageBytes, b = a + kABytes;
                 const int row = (int)(r0 + (int64_t)u * kTK);
-                mbar_arrive_expect_tx(bar(kFull + s), kStageBytes);
-                for (int i = 0; i < kTM / 64; ++i)
+                mbar_arrive_expect_tx(bar(kFull + s), kBBytes + a_boxes * kBoxBytes);
+                for (int i = 0; i < a_boxes; ++i)
                     tma_load_2d(a + i * kBoxBytes, &mx, m0 + i * 64, row, bar(kFull + s));
                 for (int i = 0; i < kTN / 64; ++i)
                     tma_load_2d(b + i * kBoxBytes, proj ? &mu : &mg, n0 + i * 64, row,
@@ -99,7 +104,7 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         }
     } else if (warp == 1) {
         // both operands MN-major (bits 15 and 16): K runs down the rows of a box
-        constexpr uint32_t idesc = idesc_f32acc(kTM, kTN, 1) | (1u << 15) | kBMajorMN;
+        constexpr uint32_t idesc = idesc_f32acc(128, kTN, 1) | (1u << 15) | kBMajorMN;
         for (int u = 0; u < steps; ++u) {
             const int s = u % kStages;
             if (!warp_wait(bar(kFull + s), (u / kStages) & 1, ab)) break;
@@ -112,6 +117,12 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
                 for (int kk = 0; kk < kTK / 16; ++kk)
                     mma_ss<false>(tmem, desc_add(ad, kk * 2048), desc_add(bd, kk * 2048), idesc,
                                   (u > 0 || kk > 0) ? 1u : 0u);
+                if (second)
+#pragma unroll
+                    for (int kk = 0; kk < kTK / 16; ++kk)
+                        mma_ss<false>(tmem + 256, desc_add(ad, 2 * kBoxBytes + kk * 2048),
+                                      desc_add(bd, kk * 2048), idesc,
+                                      (u > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(bar(kEmpty + s));
             }
             __syncwarp();
@@ -123,7 +134,8 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     } else {
         const int quad = warp & 3, t = (warp - 2) * 32 + lane;
         float *part = g.part + (size_t)split * g.part_floats;
-        if (sums) {
+        const int half = (warp - 2) >> 2;
+        if (sums && half == 0) {
             // columns 2t and 2t + 1 of the d tile, rows in order
             float s0 = 0.f, s1 = 0.f;
             const int col = 2 * t, box = col / 64, inb = (col % 64) * 2;
@@ -155,13 +167,13 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         }
         done = warp_wait(bar(kDone), 0, ab);
         tc_fence_after();
-        if (done) {
-            const int row = m0 + quad * 32 + lane;
+        if (done && (half == 0 || second)) {
+            const int row = m0 + half * 128 + quad * 32 + lane;
             float *dst = part + ((size_t)proj * g.din + row) * g.dout + n0;
             for (int cg = 0; cg < kTN / 32; ++cg) {
                 if (n0 + cg * 32 >= g.dout) break;
                 uint32_t v[32];
-                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + cg * 32, v);
+                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + half * 256 + cg * 32, v);
                 if (row < g.din) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
@@ -176,13 +188,15 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 256);
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 // ---- contraction with the factors ----
+// dW is read as float4 along k, twice (second time from L2): once with a block per few (a, c)
+// for dC, once with a thread per four (j, k) for dB.
 constexpr int kCt = 256;      // threads
 constexpr int kRc = 8;        // ranks summed at a time
-constexpr int kCc = 4;        // columns c per warp (dC)
+constexpr int kJs = 4;        // parts of j (dC)
 
 struct CtArgs {
     const float *part;
@@ -192,100 +206,125 @@ struct CtArgs {
     __nv_bfloat16 *dS, *dA;
     float *dbp;                  // [dbs][2][r][m1][m2]
     int p, q, m1, m2, r, dout, dbs;
+    int tk, cpb;                 // threads along k (m2 / 4), columns c per block (dC)
     int dc_blocks;               // blocks of the first role
 };
 
-__device__ __forceinline__ float dw_sum(const CtArgs &g, size_t o) {
-    float v = __ldg(g.part + o);
-    for (int s = 1; s < g.splits; ++s) v += __ldg(g.part + (size_t)s * g.part_floats + o);
+__device__ __forceinline__ float4 dw4(const CtArgs &g, size_t o) {
+    float4 v = __ldg(reinterpret_cast<const float4 *>(g.part + o));
+    for (int s = 1; s < g.splits; ++s) {
+        const float4 w =
+            __ldg(reinterpret_cast<const float4 *>(g.part + (size_t)s * g.part_floats + o));
+        v.x += w.x;
+        v.y += w.y;
+        v.z += w.z;
+        v.w += w.w;
+    }
     return v;
 }
 
-// dC, dA, dS: a warp per (projection, a, four columns c)
+// dC, dA, dS: a block per (projection, a, cpb columns c); a thread has four k of one c and a
+// quarter of the j, and the threads of one c are added in order.
 __device__ void dc_role(const CtArgs &g) {
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * (kCt / 32) + (threadIdx.x >> 5);
-    const int ncg = cdiv(g.q, kCc);
-    if (w >= (int64_t)2 * g.p * ncg) return;
-    const int c0 = (int)(w % ncg) * kCc, a = (int)(w / ncg % g.p), proj = (int)(w / ncg / g.p);
-    const size_t row0 = ((size_t)proj * g.p + a) * g.m1;   // rows of dW: (proj, a, j)
-    float ds[kCc] = {};
+    __shared__ float acc_s[kRc][kCt];
+    const int ncb = cdiv(g.q, g.cpb), blk = blockIdx.x;
+    const int c0 = blk % ncb * g.cpb, a = blk / ncb % g.p, proj = blk / ncb / g.p;
+    const int kk = threadIdx.x % g.tk, rest = threadIdx.x / g.tk;
+    const int cl = rest % g.cpb, js = rest / g.cpb;
+    const bool live = js < kJs && c0 + cl < g.q;
+    const int per_j = cdiv(g.m1, kJs), j0 = js * per_j, j1 = min(g.m1, j0 + per_j);
+    const size_t o0 = ((size_t)proj * g.p + a) * g.m1 * g.dout + (size_t)(c0 + cl) * g.m2 + 4 * kk;
+    const size_t mm = (size_t)g.m1 * g.m2, pq = (size_t)g.p * g.q;
+    float ds = 0.f;
     for (int i0 = 0; i0 < g.r; i0 += kRc) {
-        float acc[kCc][kRc] = {};
-        const __nv_bfloat16 *Bi = g.B + ((size_t)proj * g.r + i0) * g.m1 * g.m2;
         const int ni = min(kRc, g.r - i0);
-        for (int e = lane; e < g.m1 * g.m2; e += 32) {
-            const int j = e / g.m2, k = e - j * g.m2;
-            const size_t o = (row0 + j) * g.dout + (size_t)c0 * g.m2 + k;
-            float v[kCc];
-#pragma unroll
-            for (int t = 0; t < kCc; ++t)
-                v[t] = c0 + t < g.q ? dw_sum(g, o + (size_t)t * g.m2) : 0.f;
-#pragma unroll
-            for (int i = 0; i < kRc; ++i) {
-                const float b =
-                    i < ni ? __bfloat162float(Bi[(size_t)i * g.m1 * g.m2 + e]) : 0.f;
-#pragma unroll
-                for (int t = 0; t < kCc; ++t) acc[t][i] = fmaf(v[t], b, acc[t][i]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < kCc; ++t)
-#pragma unroll
-            for (int i = 0; i < kRc; ++i)
-                for (int o = 16; o; o >>= 1)
-                    acc[t][i] += __shfl_xor_sync(0xffffffffu, acc[t][i], o);
-        if (lane == 0) {
-            for (int t = 0; t < kCc && c0 + t < g.q; ++t) {
-                const size_t pos = (size_t)a * g.q + c0 + t, pq = (size_t)g.p * g.q;
-                const float s = __bfloat162float(g.S[proj * pq + pos]);
+        float acc[kRc] = {};
+        if (live) {
+            const __nv_bfloat16 *Bi = g.B + ((size_t)proj * g.r + i0) * mm + 4 * kk;
+#pragma unroll 2
+            for (int j = j0; j < j1; ++j) {
+                const float4 v = dw4(g, o0 + (size_t)j * g.dout);
 #pragma unroll
                 for (int i = 0; i < kRc; ++i)
                     if (i < ni) {
-                        const size_t ai = ((size_t)proj * g.r + i0 + i) * pq + pos;
-                        g.dA[ai] = __float2bfloat16_rn(acc[t][i] * s);
-                        ds[t] = fmaf(acc[t][i], __bfloat162float(g.A[ai]), ds[t]);
+                        const uint2 w = __ldg(
+                            reinterpret_cast<const uint2 *>(Bi + i * mm + (size_t)j * g.m2));
+                        acc[i] = fmaf(v.x, __uint_as_float(w.x << 16), acc[i]);
+                        acc[i] = fmaf(v.y, __uint_as_float(w.x & 0xFFFF0000u), acc[i]);
+                        acc[i] = fmaf(v.z, __uint_as_float(w.y << 16), acc[i]);
+                        acc[i] = fmaf(v.w, __uint_as_float(w.y & 0xFFFF0000u), acc[i]);
                     }
             }
         }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kRc; ++i) acc_s[i][threadIdx.x] = acc[i];
+        __syncthreads();
+        // thread (i, c): the sum of its c's threads in order, into the first of them
+        for (int e = threadIdx.x; e < ni * g.cpb; e += kCt) {
+            const int i = e / g.cpb, c = e % g.cpb;
+            float v = 0.f;
+            for (int u = 0; u < kJs; ++u)
+                for (int t = 0; t < g.tk; ++t) v += acc_s[i][(u * g.cpb + c) * g.tk + t];
+            acc_s[i][c * g.tk] = v;
+            if (c0 + c < g.q) {
+                const size_t pos = (size_t)a * g.q + c0 + c;
+                g.dA[((size_t)proj * g.r + i0 + i) * pq + pos] =
+                    __float2bfloat16_rn(v * __bfloat162float(g.S[proj * pq + pos]));
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x < g.cpb && c0 + (int)threadIdx.x < g.q)
+            for (int i = 0; i < ni; ++i)
+                ds = fmaf(acc_s[i][threadIdx.x * g.tk],
+                          __bfloat162float(g.A[((size_t)proj * g.r + i0 + i) * pq +
+                                               (size_t)a * g.q + c0 + threadIdx.x]),
+                          ds);
     }
-    if (lane == 0)
-        for (int t = 0; t < kCc && c0 + t < g.q; ++t)
-            g.dS[(size_t)proj * g.p * g.q + (size_t)a * g.q + c0 + t] = __float2bfloat16_rn(ds[t]);
+    if (threadIdx.x < g.cpb && c0 + (int)threadIdx.x < g.q)
+        g.dS[proj * pq + (size_t)a * g.q + c0 + threadIdx.x] = __float2bfloat16_rn(ds);
 }
 
-// dB partial sums: a thread per (j, k), a block per (projection, range of a, ranks)
+// dB partial sums: a thread per four (j, k), a block per (projection, range of (a, c), ranks)
 __device__ void db_role(const CtArgs &g, int blk) {
-    extern __shared__ float cs[];      // C_i[a][.] of one a: [kRc][q]
-    const int eb = cdiv(g.m1 * g.m2, kCt), ib = cdiv(g.r, kRc);
-    const int e = (blk % eb) * kCt + threadIdx.x;
+    __shared__ float cs[kRc][64];      // C_i of up to 64 (a, c)
+    const int n4 = g.m1 * g.tk, eb = cdiv(n4, kCt), ib = cdiv(g.r, kRc);
+    const int e = blk % eb * kCt + threadIdx.x;
     blk /= eb;
     const int i0 = (blk % ib) * kRc;
     blk /= ib;
     const int range = blk % g.dbs, proj = blk / g.dbs;
-    const int ni = min(kRc, g.r - i0);
-    const int a0 = (int)((int64_t)g.p * range / g.dbs), a1 = (int)((int64_t)g.p * (range + 1) / g.dbs);
-    const bool live = e < g.m1 * g.m2;
-    const int j = live ? e / g.m2 : 0, k = live ? e - j * g.m2 : 0;
-    float acc[kRc] = {};
-    const size_t pq = (size_t)g.p * g.q;
-    for (int a = a0; a < a1; ++a) {
+    const int ni = min(kRc, g.r - i0), pq = g.p * g.q;
+    const int f0 = (int)((int64_t)pq * range / g.dbs), f1 = (int)((int64_t)pq * (range + 1) / g.dbs);
+    const bool live = e < n4;
+    const int j = live ? e / g.tk : 0, k = live ? 4 * (e - j * g.tk) : 0;
+    float acc[kRc][4] = {};
+    for (int f = f0; f < f1; f += 64) {
+        const int nf = min(64, f1 - f);
         __syncthreads();
-        for (int u = threadIdx.x; u < kRc * g.q; u += kCt) {
-            const int i = u / g.q, c = u - i * g.q;
-            const size_t pos = (size_t)a * g.q + c;
-            cs[u] = i < ni ? __bfloat162float(g.S[proj * pq + pos]) *
-                                 __bfloat162float(g.A[((size_t)proj * g.r + i0 + i) * pq + pos])
+        for (int u = threadIdx.x; u < kRc * 64; u += kCt) {
+            const int i = u >> 6, w = u & 63;
+            cs[i][w] = i < ni && w < nf
+                           ? __bfloat162float(g.S[(size_t)proj * pq + f + w]) *
+                                 __bfloat162float(g.A[((size_t)proj * g.r + i0 + i) * pq + f + w])
                            : 0.f;
         }
         __syncthreads();
         if (live) {
-            const size_t o = (((size_t)proj * g.p + a) * g.m1 + j) * g.dout + k;
+            int a = f / g.q, c = f - a * g.q;
 #pragma unroll 4
-            for (int c = 0; c < g.q; ++c) {
-                const float v = dw_sum(g, o + (size_t)c * g.m2);
+            for (int w = 0; w < nf; ++w) {
+                const float4 v = dw4(g, (((size_t)proj * g.p + a) * g.m1 + j) * g.dout +
+                                            (size_t)c * g.m2 + k);
+                if (++c == g.q) c = 0, ++a;
 #pragma unroll
-                for (int i = 0; i < kRc; ++i) acc[i] = fmaf(v, cs[i * g.q + c], acc[i]);
+                for (int i = 0; i < kRc; ++i) {
+                    const float x = cs[i][w];
+                    acc[i][0] = fmaf(v.x, x, acc[i][0]);
+                    acc[i][1] = fmaf(v.y, x, acc[i][1]);
+                    acc[i][2] = fmaf(v.z, x, acc[i][2]);
+                    acc[i][3] = fmaf(v.w, x, acc[i][3]);
+                }
             }
         }
     }
@@ -293,7 +332,10 @@ __device__ void db_role(const CtArgs &g, int blk) {
 #pragma unroll
         for (int i = 0; i < kRc; ++i)
             if (i < ni)
-                g.dbp[((((size_t)range * 2 + proj) * g.r + i0 + i) * g.m1 * g.m2) + e] = acc[i];
+                *reinterpret_cast<float4 *>(
+                    g.dbp + (((size_t)range * 2 + proj) * g.r + i0 + i) * g.m1 * g.m2 +
+                    (size_t)j * g.m2 + k) =
+                    make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
 }
 
 __global__ void __launch_bounds__(kCt) glu_contract_kernel(const CtArgs g) {
@@ -334,10 +376,11 @@ WgradPlan wgrad_plan(const Shape &s, int sms) {
     pl.splits = (int)((s.N + pl.rows_per_split - 1) / pl.rows_per_split);
     if (pl.splits < 1) pl.splits = 1;
     pl.part_floats = pad64((size_t)2 * din * dout + 2 * (size_t)dout);
-    // dB: enough ranges of a to fill the SMs about four times
-    const int64_t per = (int64_t)cdiv(s.m1 * s.m2, kCt) * cdiv(s.r, kRc) * 2;
-    int64_t dbs = (4 * sms + per - 1) / per;
-    if (dbs > s.p) dbs = s.p;
+    // dB: ranges of (a, c) for about two blocks per SM, at most 64 (their sums are added again)
+    const int64_t per = (int64_t)cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, kRc) * 2;
+    int64_t dbs = (2 * sms + per - 1) / per;
+    if (dbs > 64) dbs = 64;
+    if (dbs > (int64_t)s.p * s.q) dbs = (int64_t)s.p * s.q;
     pl.dbs = (int)dbs;
     pl.ws_bytes = 4 * (pl.part_floats * pl.splits +
                        pad64((size_t)pl.dbs * 2 * s.r * s.m1 * s.m2));
@@ -393,10 +436,14 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
     c.r = s.r;
     c.dout = dout;
     c.dbs = pl.dbs;
-    c.dc_blocks = (int)(((int64_t)2 * s.p * cdiv(s.q, kCc) + kCt / 32 - 1) / (kCt / 32));
-    const int db_blocks = cdiv(s.m1 * s.m2, kCt) * cdiv(s.r, kRc) * pl.dbs * 2;
+    c.tk = s.m2 / 4;
+    c.cpb = kCt / (c.tk * kJs);
+    if (c.cpb < 1) return cudaErrorInvalidValue;       // m2 <= 256: checked by the entry points
+    if (c.cpb > s.q) c.cpb = s.q;
+    c.dc_blocks = 2 * s.p * cdiv(s.q, c.cpb);
+    const int db_blocks = cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, kRc) * pl.dbs * 2;
     launch_step() = "factor-gradient launch";
-    glu_contract_kernel<<<(unsigned)(c.dc_blocks + db_blocks), kCt, (size_t)kRc * s.q * 4, st>>>(c);
+    glu_contract_kernel<<<(unsigned)(c.dc_blocks + db_blocks), kCt, 0, st>>>(c);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const size_t nb = (size_t)2 * s.r * s.m1 * s.m2, nbias = dbias ? (size_t)2 * dout : 0;

@@ -7,6 +7,7 @@ computes anything itself.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -367,9 +368,33 @@ def ks_backward(x, w, dY, need_dx=True, need_dbias=True, workspace=None, grads=N
     return g
 
 
-def _on(dev, name, t):
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+# Checks and launch helpers of the calls below.  A short call spends more time here than on the
+# GPU, so a tensor that is as it should be passes in one comparison.
+
+def _need(t, name, dtype, shape, dev):
+    """t is a contiguous CUDA tensor of this dtype and shape on device dev."""
+    if (t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == dev
+            and t.is_contiguous()):
+        return
+    _expect(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _on_device(dev):
+    """Context in which dev is the current device."""
+    return _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _raw_stream(stream, dev):
+    return (torch._C._cuda_getCurrentRawStream(dev.index) if stream is None
+            else stream.cuda_stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 # ---- gated half of a feed-forward block: h = act(x Wg + bg) * (x Wu + bu) ----
@@ -396,14 +421,14 @@ def _glu_args(x, S, A, B, bias, activation, dtype):
     if x.dim() != 2:
         raise ValueError(f"x must have shape (N, {p * m1}), got {tuple(x.shape)}")
     N = x.shape[0]
-    t = io_dtype(dtype)
-    _expect(x, "x", t, (N, p * m1))
-    for name, v, shp in (("S", S, (2, p, q)), ("A", A, (2, r, p, q)), ("B", B, (2, r, m1, m2)),
-                         ("bias", bias, (2, q * m2))):
-        if v is not None:
-            _expect(v, name, t, shp)
-            _on(x.device, name, v)
-    return (N, p, q, m1, m2, r), t
+    t, dev = io_dtype(dtype), x.device
+    _need(x, "x", t, (N, p * m1), dev)
+    _need(S, "S", t, (2, p, q), dev)
+    _need(A, "A", t, (2, r, p, q), dev)
+    _need(B, "B", t, (2, r, m1, m2), dev)
+    if bias is not None:
+        _need(bias, "bias", t, (2, q * m2), dev)
+    return (N, p, q, m1, m2, r), t, dev
 
 
 def glu_workspace_size(N, p, q, m1, m2, r, dtype="bf16", backward=False) -> int:
@@ -412,11 +437,16 @@ def glu_workspace_size(N, p, q, m1, m2, r, dtype="bf16", backward=False) -> int:
 
 
 def _glu_workspace(sizes, dtype, backward, workspace, dev):
-    n = glu_workspace_size(*sizes, dtype, backward)
+    """(workspace tensor to keep alive, address, bytes)"""
     if workspace is None:
-        return torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    _on(dev, "workspace", workspace)
-    return workspace
+        # the BF16 forward needs none
+        n = glu_workspace_size(*sizes, dtype, backward) if backward or dtype != "bf16" else 0
+        if not n:
+            return None, None, 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def glu_forward(x, S, A, B, bias=None, activation="silu", dtype="bf16", out=None, workspace=None,
@@ -424,17 +454,17 @@ def glu_forward(x, S, A, B, bias=None, activation="silu", dtype="bf16", out=None
     """h = act(x Wg + bg) * (x Wu + bu), W* = sum_i kron(S* (.) A*_i, B*_i); S [2][p][q],
     A [2][r][p][q], B [2][r][m1][m2] and bias [2][q*m2] hold the gate, then the up projection.
     dtype "f32" or "bf16"."""
-    sizes, t = _glu_args(x, S, A, B, bias, activation, dtype)
-    N, p, q, m1, m2, r = sizes
-    with torch.cuda.device(x.device):
+    sizes, t, dev = _glu_args(x, S, A, B, bias, activation, dtype)
+    shape = (sizes[0], sizes[2] * sizes[4])
+    with _on_device(dev):
         if out is None:
-            out = torch.empty(N, q * m2, dtype=t, device=x.device)
-        _expect(out, "h", t, (N, q * m2))
-        _on(x.device, "h", out)
-        ws = _glu_workspace(sizes, dtype, False, workspace, x.device)
-        _check(load().kron_glu_forward(_ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(out),
-                                       *sizes, ACTIVATIONS[activation], DTYPES[dtype], 0, _ptr(ws),
-                                       0 if ws is None else ws.numel(), _stream(stream)))
+            out = torch.empty(shape, dtype=t, device=dev)
+        else:
+            _need(out, "h", t, shape, dev)
+        keep, ws, ws_bytes = _glu_workspace(sizes, dtype, False, workspace, dev)
+        _check(load().kron_glu_forward(x.data_ptr(), S.data_ptr(), A.data_ptr(), B.data_ptr(),
+                                       _at(bias), out.data_ptr(), *sizes, ACTIVATIONS[activation],
+                                       DTYPES[dtype], 0, ws, ws_bytes, _raw_stream(stream, dev)))
     return out
 
 
@@ -442,44 +472,42 @@ def glu_backward(x, S, A, B, dH, bias=None, activation="silu", dtype="bf16", nee
                  need_dbias=True, workspace=None, grads=None, stream=None):
     """Gradients of <dH, h>: dict(dX, dS, dA, dB, dbias) in the tensors' own dtype (None where
     not asked).  ``grads`` may hold preallocated outputs."""
-    sizes, t = _glu_args(x, S, A, B, bias, activation, dtype)
+    sizes, t, dev = _glu_args(x, S, A, B, bias, activation, dtype)
     N, p, q, m1, m2, r = sizes
-    dev = x.device
-    _expect(dH, "dH", t, (N, q * m2))
-    _on(dev, "dH", dH)
+    _need(dH, "dH", t, (N, q * m2), dev)
     g = dict(grads or {})
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         for k, shp, need in (("dX", (N, p * m1), need_dx), ("dS", (2, p, q), True),
                              ("dA", (2, r, p, q), True), ("dB", (2, r, m1, m2), True),
                              ("dbias", (2, q * m2), need_dbias)):
             if not need:
                 g[k] = None
-                continue
-            if g.get(k) is None:
+            elif g.get(k) is None:
                 g[k] = torch.empty(shp, dtype=t, device=dev)
-            _expect(g[k], k, t, shp)
-            _on(dev, k, g[k])
-        ws = _glu_workspace(sizes, dtype, True, workspace, dev)
-        _check(load().kron_glu_backward(_ptr(x), _ptr(S), _ptr(A), _ptr(B), _ptr(bias), _ptr(dH),
-                                        _ptr(g["dX"]), _ptr(g["dS"]), _ptr(g["dA"]),
-                                        _ptr(g["dB"]), _ptr(g["dbias"]), *sizes,
-                                        ACTIVATIONS[activation], DTYPES[dtype], 0, _ptr(ws),
-                                        0 if ws is None else ws.numel(), _stream(stream)))
+            else:
+                _need(g[k], k, t, shp, dev)
+        keep, ws, ws_bytes = _glu_workspace(sizes, dtype, True, workspace, dev)
+        _check(load().kron_glu_backward(x.data_ptr(), S.data_ptr(), A.data_ptr(), B.data_ptr(),
+                                        _at(bias), dH.data_ptr(), _at(g["dX"]), _at(g["dS"]),
+                                        _at(g["dA"]), _at(g["dB"]), _at(g["dbias"]), *sizes,
+                                        ACTIVATIONS[activation], DTYPES[dtype], 0, ws, ws_bytes,
+                                        _raw_stream(stream, dev)))
     return g
 
 
 # ---- distillation loss against a teacher's top logits ----
 
-
 def _rows(t, name, dtype, N, V):
-    """A matrix whose rows are contiguous and may lie further apart than their length."""
-    if t.dtype != dtype:
+    """Row stride of a matrix whose rows are contiguous and may lie further apart than their
+    length."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (N, V):
+    if t.shape != (N, V):
         raise ValueError(f"{name} must have shape {(N, V)}, got {tuple(t.shape)}")
-    if not t.is_cuda or (V > 1 and t.stride(1) != 1) or (N > 1 and t.stride(0) < V):
+    ld, one = t.stride()
+    if not t.is_cuda or (V > 1 and one != 1) or (N > 1 and ld < V):
         raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
-    return t.stride(0) if N > 1 else V
+    return ld if N > 1 else V
 
 
 def _distill_args(logits, values, indices, labels, weights, label_weight):
@@ -489,47 +517,44 @@ def _distill_args(logits, values, indices, labels, weights, label_weight):
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     N, V = logits.shape
     K = values.shape[1]
+    dev = logits.device
     ld = _rows(logits, "logits", logits.dtype, N, V)
-    _expect(values, "values", torch.float32, (N, K))
+    _need(values, "values", torch.float32, (N, K), dev)
     if indices.dtype not in (torch.int32, torch.int64):
         raise TypeError(f"indices must be int32 or int64, got {indices.dtype}")
-    _expect(indices, "indices", indices.dtype, (N, K))
+    _need(indices, "indices", indices.dtype, (N, K), dev)
     if label_weight and labels is None:
         raise ValueError("labels are needed when label_weight is above 0")
     if labels is not None:
-        _expect(labels, "labels", torch.int64, (N,))
+        _need(labels, "labels", torch.int64, (N,), dev)
     if weights is not None:
-        _expect(weights, "weights", torch.float32, (N,))
-    for name, t in (("values", values), ("indices", indices), ("labels", labels),
-                    ("weights", weights)):
-        if t is not None:
-            _on(logits.device, name, t)
-    head = (_ptr(logits), ld, _ptr(values), _ptr(indices), indices.element_size(), _ptr(labels),
-            _ptr(weights))
-    dtype = KRON_BF16 if logits.dtype == torch.bfloat16 else KRON_F32
-    return N, V, K, head, dtype
+        _need(weights, "weights", torch.float32, (N,), dev)
+    head = (logits.data_ptr(), ld, values.data_ptr(), indices.data_ptr(),
+            8 if indices.dtype is torch.int64 else 4, _at(labels), _at(weights))
+    return N, V, K, head, KRON_BF16 if logits.dtype is torch.bfloat16 else KRON_F32, dev
 
 
 def _dlogits(logits, out):
     N, V = logits.shape
     if out is None:
-        out = torch.empty(N, V, dtype=logits.dtype, device=logits.device)
+        return torch.empty(N, V, dtype=logits.dtype, device=logits.device), V
     ld = _rows(out, "dlogits", logits.dtype, N, V)
-    _on(logits.device, "dlogits", out)
+    if out.device != logits.device:
+        raise ValueError(f"dlogits is on {out.device}, not on {logits.device}")
     return out, ld
 
 
 def distill_forward(logits, values, indices, labels=None, weights=None, temperature=1.0,
                     label_weight=0.0, stream=None):
     """Loss of each row against the teacher's top logits: dict(loss [N], lse [N][2])."""
-    N, V, K, head, dtype = _distill_args(logits, values, indices, labels, weights, label_weight)
-    dev = logits.device
-    with torch.cuda.device(dev):
+    N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
+                                              label_weight)
+    with _on_device(dev):
         loss = torch.empty(N, dtype=torch.float32, device=dev)
         lse = torch.empty(N, 2, dtype=torch.float32, device=dev)
-        _check(load().kron_distill_forward(*head, _ptr(loss), _ptr(lse), N, V, K,
-                                           float(temperature), float(label_weight), dtype,
-                                           _stream(stream)))
+        _check(load().kron_distill_forward(*head, loss.data_ptr(), lse.data_ptr(), N, V, K,
+                                           temperature, label_weight, dtype,
+                                           _raw_stream(stream, dev)))
     return {"loss": loss, "lse": lse}
 
 
@@ -537,17 +562,16 @@ def distill_backward(logits, values, indices, lse, dloss=None, labels=None, weig
                      temperature=1.0, label_weight=0.0, out=None, stream=None):
     """Gradient of <dloss, loss> in the logits (``dloss`` None: ones).  ``out`` may be the
     logits themselves, which the gradient then overwrites."""
-    N, V, K, head, dtype = _distill_args(logits, values, indices, labels, weights, label_weight)
-    dev = logits.device
-    for name, t, shp in (("lse", lse, (N, 2)), ("dloss", dloss, (N,))):
-        if t is not None:
-            _expect(t, name, torch.float32, shp)
-            _on(dev, name, t)
-    with torch.cuda.device(dev):
+    N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
+                                              label_weight)
+    _need(lse, "lse", torch.float32, (N, 2), dev)
+    if dloss is not None:
+        _need(dloss, "dloss", torch.float32, (N,), dev)
+    with _on_device(dev):
         out, ld_out = _dlogits(logits, out)
-        _check(load().kron_distill_backward(*head, _ptr(lse), _ptr(dloss), _ptr(out), ld_out, N, V,
-                                            K, float(temperature), float(label_weight), dtype,
-                                            _stream(stream)))
+        _check(load().kron_distill_backward(*head, lse.data_ptr(), _at(dloss), out.data_ptr(),
+                                            ld_out, N, V, K, temperature, label_weight, dtype,
+                                            _raw_stream(stream, dev)))
     return out
 
 
@@ -555,12 +579,12 @@ def distill_step(logits, values, indices, labels=None, weights=None, temperature
                  label_weight=0.0, out=None, stream=None):
     """Loss of each row and the gradient of their sum, the logits read once:
     dict(loss [N], dlogits).  ``out`` may be the logits themselves."""
-    N, V, K, head, dtype = _distill_args(logits, values, indices, labels, weights, label_weight)
-    dev = logits.device
-    with torch.cuda.device(dev):
+    N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
+                                              label_weight)
+    with _on_device(dev):
         loss = torch.empty(N, dtype=torch.float32, device=dev)
         out, ld_out = _dlogits(logits, out)
-        _check(load().kron_distill_step(*head, _ptr(loss), _ptr(out), ld_out, N, V, K,
-                                        float(temperature), float(label_weight), dtype,
-                                        _stream(stream)))
+        _check(load().kron_distill_step(*head, loss.data_ptr(), out.data_ptr(), ld_out, N, V, K,
+                                        temperature, label_weight, dtype,
+                                        _raw_stream(stream, dev)))
     return {"loss": loss, "dlogits": out}
