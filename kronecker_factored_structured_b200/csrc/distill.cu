@@ -6,12 +6,16 @@
 //   loss = w [ (1 - lam) tau^2 sum_j p_j (log p_j - log q_{i_j}) + lam (lse(x) - x_label) ]
 //   dx_v = w dl [ (1 - lam) tau (q_v - sum_{j: i_j = v} p_j) + lam (softmax(x)_v - [v = label]) ]
 //
-// One CTA per row.  Pass 1 reads the row once with a running maximum m and the sums of
-// exp((x - m)/tau) and exp(x - m) per thread; pass 2 (gradient) reads it again, from L2, and
-// writes the dense part c_t q + c_1 softmax(x); the K + 1 columns that the teacher and the
-// label touch are then overwritten by the thread that owns the first entry of the column,
+// One CTA of 256 threads per row, six per SM.  Pass 1 reads the row with a running maximum m per
+// thread and the sums of exp((x - m)/tau) and exp(x - m); pass 2 (gradient) reads it again, from
+// L2, and writes the dense part c_t q + c_1 softmax(x); the K + 1 columns that the teacher and
+// the label touch are then overwritten by the thread that owns the first entry of the column,
 // in fp32, from logits fetched before anything is written (so dlogits may be the logits).
-// Bound: HBM (one read, one write of the logits); per element one or two ex2.
+// Bound: HBM moves the logits once in and once out (126 us for 4096 x 50257 bf16); per element
+// and pass one ex2 (two for a tau other than 1, 2 and 4), 92 us on the special-function units,
+// and with the packed FP32 instructions some 11 issue slots.  Measured 177 us (scalar FP32
+// instructions: 191; 512 threads, three CTAs per SM: 212; rows split over clusters of four
+// CTAs and held in registers, one read: 301, the barriers of the shorter pieces not covered).
 #include "../../include/kron_linear.h"
 #include "internal.h"
 
@@ -25,7 +29,7 @@ kron_status_t report_failure(kron_status_t st, const char *msg);
 namespace {
 
 constexpr int kMaxK = 1024;      // teacher entries per row
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -60,40 +64,83 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
+// Two fp32 values in one 64-bit register pair, for the packed FP32 instructions: one issue slot
+// for two additions, multiplications or multiply-adds, each rounded as the scalar one.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return pack2(ex2(lo), ex2(hi));
+}
+
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int n = 4;
-    static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[4]) {
-        f[0] = __uint_as_float(u.x);
-        f[1] = __uint_as_float(u.y);
-        f[2] = __uint_as_float(u.z);
-        f[3] = __uint_as_float(u.w);
+    static __device__ __forceinline__ void unpack(const uint4 &u, f2 (&f)[2]) {
+        f[0] = pack2(__uint_as_float(u.x), __uint_as_float(u.y));
+        f[1] = pack2(__uint_as_float(u.z), __uint_as_float(u.w));
     }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
+    static __device__ __forceinline__ uint4 pack(const f2 (&f)[2]) {
+        float a, b, c, d;
+        unpack2(f[0], a, b);
+        unpack2(f[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c),
+                          __float_as_uint(d));
+    }
+    // the largest of the vector's values (a NaN only where all are)
+    static __device__ __forceinline__ float max(const uint4 &u) {
+        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)),
+                     fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
     }
     static __device__ __forceinline__ float get(const float *p) { return *p; }
     static __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int n = 8;
-    static __device__ __forceinline__ void unpack(const uint4 &u, float (&f)[8]) {
+    static __device__ __forceinline__ void unpack(const uint4 &u, f2 (&f)[4]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 4; ++i)
+            f[i] = pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+    static __device__ __forceinline__ uint4 pack(const f2 (&f)[4]) {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            float lo, hi;
+            unpack2(f[i], lo, hi);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
             w[i] = *reinterpret_cast<const uint32_t *>(&h);
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ float max(const uint4 &u) {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
     }
     static __device__ __forceinline__ float get(const __nv_bfloat16 *p) {
         return __bfloat162float(*p);
@@ -157,7 +204,7 @@ template <int E> __device__ __forceinline__ Stat shuffle_xor(const Stat &st, int
 // What a row needs of the teacher, in shared memory: columns (-1: no entry), probabilities,
 // student logits at the columns.
 struct RowSmem {
-    int col[kMaxK];
+    alignas(16) int col[kMaxK + 4];
     float prob[kMaxK];
     float x[kMaxK];
     Stat warp[32];
@@ -188,7 +235,7 @@ __device__ __forceinline__ float block_max(float v, float *red) {
 }
 
 template <typename T, int E, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(kThreads) distill_kernel(const Args g) {
+__global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const Args g) {
     __shared__ RowSmem sm;
     using Vc = Vec<T>;
     constexpr int n = Vc::n;
@@ -224,14 +271,19 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const Args g) {
 
     // ---- the teacher's distribution over the row's entries
     float tm = -INFINITY;
-    for (int j = tid; j < K; j += kThreads) {
-        const int64_t i = g.idx64 ? static_cast<const int64_t *>(g.indices)[row * K + j]
-                                  : static_cast<const int *>(g.indices)[row * K + j];
+    const int Kp = (K + 3) & ~3;
+    for (int j = tid; j < Kp; j += kThreads) {
+        int64_t i = -1;
+        if (j < K)
+            i = g.idx64 ? static_cast<const int64_t *>(g.indices)[row * K + j]
+                        : static_cast<const int *>(g.indices)[row * K + j];
         const bool there = i >= 0 && i < V;
         const float t = there ? g.values[row * K + j] : -INFINITY;
         sm.col[j] = there ? (int)i : -1;
-        sm.prob[j] = t;
-        sm.x[j] = there ? Vc::get(x + i) : 0.f;
+        if (j < K) {
+            sm.prob[j] = t;
+            sm.x[j] = there ? Vc::get(x + i) : 0.f;
+        }
         tm = fmaxf(tm, t);
     }
     const int64_t lab64 = g.labels ? g.labels[row] : -1;
@@ -239,11 +291,27 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const Args g) {
     const float xlab = label >= 0 ? Vc::get(x + label) : 0.f;
     tm = block_max(tm, sm.redm);
     float ts = 0.f;
+    bool twice = false, listed = false;   // a column listed twice; the label's column listed
     for (int j = tid; j < K; j += kThreads) {
         const float t = sm.prob[j];
         const float e = t == -INFINITY ? 0.f : ex2((t - tm) * (kLog2e / g.tau));
         sm.prob[j] = e;
         ts += e;
+        listed = listed || (label >= 0 && sm.col[j] == label);
+    }
+    if constexpr (GRAD) {
+        // all threads share the pairs: thread tid has entry j = tid % step and every G-th four
+        // of the entries before it
+        for (int j0 = 0; j0 < K; j0 += kThreads) {
+            const int step = min(K - j0, kThreads), G = kThreads / step;
+            const int j = j0 + tid % step, part = tid / step, c = sm.col[j];
+            if (part < G && c >= 0)
+                for (int k = 4 * part; k < j; k += 4 * G) {
+                    const int4 o = *reinterpret_cast<const int4 *>(sm.col + k);
+                    twice = twice || o.x == c || (o.y == c && k + 1 < j) ||
+                            (o.z == c && k + 2 < j) || (o.w == c && k + 3 < j);
+                }
+        }
     }
     ts = block_sum(ts, sm.red);
     const bool any = ts != 0.f;   // NaN counts: it has to show
@@ -253,21 +321,52 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const Args g) {
     float lse_t, lse_1;
     if constexpr (STATS) {
         Stat st{-INFINITY, 0.f, 0.f};
-        for (int v = tid; v < nv; v += kThreads) {
-            float f[n];
-            Vc::unpack(xv[v], f);
-            float m = f[0];
-#pragma unroll
-            for (int i = 1; i < n; ++i) m = fmaxf(m, f[i]);
-            rebase<E>(st, m, a);
-            const float base = st.m == -INFINITY ? 0.f : st.m;
-#pragma unroll
-            for (int i = 0; i < n; ++i) {
-                const float d = f[i] - base;
-                const float e = ex2(d * a);
-                st.s += e;
-                if constexpr (E != kOne) st.s1 += second<E>(e, d);
+        // sums of the thread's even and odd elements, relative to st.m
+        f2 sum = pack2(0.f, 0.f), sum1 = sum;
+        const f2 a2 = pack2(a, a), l2 = pack2(kLog2e, kLog2e);
+        auto add_vec = [&](const uint4 &u) {
+            const float m = Vc::max(u);
+            if (m > st.m) {
+                const float d = st.m - m, e = ex2(d * a);
+                sum = mul2(sum, pack2(e, e));
+                if constexpr (E != kOne) {
+                    const float e1 = second<E>(e, d);
+                    sum1 = mul2(sum1, pack2(e1, e1));
+                }
+                st.m = m;
             }
+            const float base = st.m == -INFINITY ? 0.f : -st.m;
+            const f2 b2 = pack2(base, base);
+            f2 f[n / 2];
+            Vc::unpack(u, f);
+#pragma unroll
+            for (int i = 0; i < n / 2; ++i) {
+                const f2 d = add2(f[i], b2);      // exact next to the maximum, however large
+                const f2 e = ex2_2(mul2(d, a2));
+                sum = add2(sum, e);
+                if constexpr (E == kSquare) sum1 = fma2(e, e, sum1);
+                if constexpr (E == kFourth) {
+                    const f2 q = mul2(e, e);
+                    sum1 = fma2(q, q, sum1);
+                }
+                if constexpr (E == kTwo) sum1 = add2(sum1, ex2_2(mul2(d, l2)));
+            }
+        };
+        int v = tid;
+        for (; v + 3 * kThreads < nv; v += 4 * kThreads) {
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = xv[v + i * kThreads];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) add_vec(u[i]);
+        }
+        for (; v < nv; v += kThreads) add_vec(xv[v]);
+        {
+            float lo, hi;
+            unpack2(sum, lo, hi);
+            st.s = lo + hi;
+            unpack2(sum1, lo, hi);
+            st.s1 = lo + hi;
         }
         if (tid < head) add_one<E>(st, Vc::get(x + tid), a);
         const int tail = head + nv * n + tid;
@@ -318,55 +417,79 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(const Args g) {
     const float hard = g.lam != 0.f && label >= 0 ? coef * g.lam : 0.f;
     const float c_t = E == kOne ? soft + hard : soft;
     const float b_t = -lse_t * kLog2e, b_1 = -lse_1 * kLog2e;
-    // exp(x - lse_1) from q: (q exp(lse_t - lse_1/tau))^tau, the factor in [1, V]
+    // exp(x - lse_1) from q: (q exp(lse_t - lse_1/tau))^tau, the factor in [1, V]; with its power
+    // in the coefficient: hard lift^tau q^tau
     const float lift = E == kSquare ? ex2((lse_t - 0.5f * lse_1) * kLog2e)
                                     : E == kFourth ? ex2((lse_t - 0.25f * lse_1) * kLog2e) : 1.f;
-    auto dense = [&](float v) {
-        const float e = ex2(fmaf(v, a, b_t));
-        float d = c_t == 0.f ? 0.f : c_t * e;
-        if constexpr (E == kSquare || E == kFourth) {
-            const float f = e * lift, f2 = f * f;
-            d = fmaf(hard, E == kSquare ? f2 : f2 * f2, d);
-        }
-        if constexpr (E == kTwo) d = fmaf(hard, ex2(fmaf(v, kLog2e, b_1)), d);
-        return d;
+    const float lift2 = lift * lift;
+    const float c_1 = E == kSquare ? hard * lift2 : E == kFourth ? hard * (lift2 * lift2) : hard;
+    // q (c_t + c_1 q^(tau - 1)) and so on, for two elements
+    const f2 a2 = pack2(a, a), b2 = pack2(b_t, b_t), ct2 = pack2(c_t, c_t), c12 = pack2(c_1, c_1);
+    auto dense2 = [&](f2 v) {
+        const f2 e = ex2_2(fma2(v, a2, b2));
+        if constexpr (E == kOne) return mul2(ct2, e);
+        if constexpr (E == kSquare) return mul2(e, fma2(c12, e, ct2));
+        if constexpr (E == kFourth) return mul2(e, fma2(mul2(c12, e), mul2(e, e), ct2));
+        const f2 l2 = pack2(kLog2e, kLog2e), d2 = pack2(b_1, b_1);
+        return fma2(c12, ex2_2(fma2(v, l2, d2)), mul2(ct2, e));
     };
-    __syncthreads();   // every gather of the row is done before it may be overwritten
-    for (int v = tid; v < nv; v += kThreads) {
-        float f[n];
-        Vc::unpack(xv[v], f);
+    auto dense = [&](float v) {
+        float lo, hi;
+        unpack2(dense2(pack2(v, v)), lo, hi);
+        return lo;
+    };
+    // every gather of the row is done before it may be overwritten
+    const bool dup = __syncthreads_or(twice), has_label = __syncthreads_or(listed);
+    auto grad_vec = [&](const uint4 &u, int v) {
+        f2 f[n / 2];
+        Vc::unpack(u, f);
 #pragma unroll
-        for (int i = 0; i < n; ++i) f[i] = dense(f[i]);
+        for (int i = 0; i < n / 2; ++i) f[i] = dense2(f[i]);
         T *o = out + head + v * n;
         if (same) {
-            *reinterpret_cast<uint4 *>(o) = Vc::pack(f);
+            __stcs(reinterpret_cast<uint4 *>(o), Vc::pack(f));
         } else {
 #pragma unroll
-            for (int i = 0; i < n; ++i) Vc::put(o + i, f[i]);
+            for (int i = 0; i < n / 2; ++i) {
+                float lo, hi;
+                unpack2(f[i], lo, hi);
+                Vc::put(o + 2 * i, lo);
+                Vc::put(o + 2 * i + 1, hi);
+            }
         }
+    };
+    int v = tid;
+    for (; v + 3 * kThreads < nv; v += 4 * kThreads) {
+        uint4 u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = __ldcs(xv + v + i * kThreads);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) grad_vec(u[i], v + i * kThreads);
     }
+    for (; v < nv; v += kThreads) grad_vec(__ldcs(xv + v), v);
     if (tid < head) Vc::put(out + tid, dense(Vc::get(x + tid)));
     const int tail = head + nv * n + tid;
     if (tail < V) Vc::put(out + tail, dense(Vc::get(x + tail)));
     __syncthreads();
+    const float share = soft == 0.f ? 0.f : soft * its;
     for (int j = tid; j < K; j += kThreads) {
         const int c = sm.col[j];
         if (c < 0) continue;
-        float p = 0.f;
+        float p = sm.prob[j];
         bool first = true;      // a column listed more than once: its first entry writes it
-        for (int k = 0; k < K; ++k)
-            if (sm.col[k] == c) {
-                if (k < j) first = false;
-                p += sm.prob[k];
-            }
-        const float teacher = soft == 0.f ? 0.f : soft * its * p;
-        if (first) Vc::put(out + c, dense(sm.x[j]) - teacher - (c == label ? hard : 0.f));
+        if (dup) {
+            p = 0.f;
+            for (int k = 0; k < K; ++k)
+                if (sm.col[k] == c) {
+                    if (k < j) first = false;
+                    p += sm.prob[k];
+                }
+        }
+        if (first)
+            Vc::put(out + c, dense(sm.x[j]) - (share == 0.f ? 0.f : share * p) -
+                                 (c == label ? hard : 0.f));
     }
-    if (tid == 0 && label >= 0) {
-        bool listed = false;
-        for (int k = 0; k < K; ++k) listed = listed || sm.col[k] == label;
-        if (!listed) Vc::put(out + label, dense(xlab) - hard);
-    }
+    if (tid == 0 && label >= 0 && !has_label) Vc::put(out + label, dense(xlab) - hard);
 }
 
 kron_status_t bad(kron_status_t st, const char *fmt, double a = 0, double b = 0) {
