@@ -5,9 +5,10 @@
 //   du = dH act(g),  dg = dH u act'(g);  each projection's gradients as the layer's
 //
 // BF16: one tensor-core kernel forward; backward: the pre-activations' gradients, dX, the dense
-// weight gradients and their contraction (glu_tc.cu, glu_wgrad.cu).  F32: the layer's exact
-// CUDA-core kernels for both projections with the elementwise kernels below between them, FFMA
-// bound: the elementwise passes move 12 to 20 bytes per element of h.
+// weight gradients and their contraction (glu_tc.cu, glu_wgrad.cu).  F32: one CUDA-core kernel
+// for both projections and the activation (simt_f32.cu), or the layer's kernels for each with the
+// elementwise kernels below; backward by the layer's kernels over both projections at once; FFMA
+// bound.
 #include "glu.h"
 
 #include <math.h>
@@ -36,31 +37,6 @@ kron_status_t cuda_bad(cudaError_t e, const char *what) {
     return bad(KRON_ERR_CUDA, "%s (%s): %s", what, launch_step(), cudaGetErrorString(e));
 }
 
-// act(g) and act'(g) with the accurate functions (exact-FP32 path).
-__device__ __forceinline__ float act_f32(int act, float g, float *d) {
-    if (act == KRON_ACT_GELU) {
-        const float c = 0.5f * erfcf(-g * 0.70710678118654752f);
-        const float e = expf(-0.5f * g * g);
-        *d = c + (e == 0.f ? 0.f : g * e * 0.39894228040143268f);
-        return g * c;
-    }
-    if (act == KRON_ACT_GELU_TANH) {
-        const float g2 = g * g;
-        const float v = 1.5957691216057308f * g * (1.f + 0.044715f * g2);
-        const float s = 1.f / (1.f + expf(-v)), w = s * (1.f / (1.f + expf(v)));
-        *d = s + (w == 0.f ? 0.f : g * w * 1.5957691216057308f * (1.f + 0.134145f * g2));
-        return g * s;
-    }
-    const float s = 1.f / (1.f + expf(-g)), c = 1.f / (1.f + expf(g));   // c = 1 - s
-    if (act == KRON_ACT_SIGMOID) {
-        *d = s * c;
-        return s;
-    }
-    const float f = g * s;
-    *d = s + f * c;
-    return f;
-}
-
 // h = act(g) * u, in place of u.
 __global__ void gate_f32_kernel(const float4 *g, float4 *u, int64_t n4, int act) {
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < n4;
@@ -68,10 +44,10 @@ __global__ void gate_f32_kernel(const float4 *g, float4 *u, int64_t n4, int act)
         const float4 a = g[i];
         float4 b = u[i];
         float d;
-        b.x *= act_f32(act, a.x, &d);
-        b.y *= act_f32(act, a.y, &d);
-        b.z *= act_f32(act, a.z, &d);
-        b.w *= act_f32(act, a.w, &d);
+        b.x *= glu::act_f32(act, a.x, &d);
+        b.y *= glu::act_f32(act, a.y, &d);
+        b.z *= glu::act_f32(act, a.z, &d);
+        b.w *= glu::act_f32(act, a.w, &d);
         u[i] = b;
     }
 }
@@ -87,7 +63,7 @@ __global__ void gate_grad_f32_kernel(float4 *g, float4 *u, const float4 *dh, int
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             float d;
-            const float f = act_f32(act, pa[t], &d);
+            const float f = glu::act_f32(act, pa[t], &d);
             pa[t] = ph[t] * pb[t] * d;
             pb[t] = ph[t] * f;
         }
@@ -152,15 +128,23 @@ kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int ac
     return KRON_OK;
 }
 
-// Workspace: forward F32 [g]; backward F32 [g][u][dX of up][partials of one projection];
+// F32: whether both projections run in one kernel with the activation.  The compiled shape's own
+// kernels are faster than that one where they have rows to fill the SMs with: 20000 rows, r = 4,
+// MEASURE_FUSED us in one kernel and MEASURE_TWO us in two and an elementwise pass.
+bool fused_f32(const Shape &s) {
+    const bool compiled = s.p == 32 && s.q == 32 && s.m1 == 32 && s.m2 == 32 && s.r == 4;
+    return glu::simt_pre_supported(s) && !(compiled && s.N >= 8 * 2 * kRowParts);
+}
+
+// Workspace: forward F32 [g] unless fused; backward F32 [g][u][dX of up][partials of both];
 // backward BF16 [dg][du][weight gradients].
 size_t need_bytes(const Shape &s, kron_dtype_t dtype, bool backward) {
     const size_t h = (size_t)s.N * s.d_out(), x = (size_t)s.N * s.d_in();
     if (dtype == KRON_BF16)
         return backward ? 2 * pad256(2 * h) + glu::wgrad_plan(s, kRowParts).ws_bytes : 0;
-    if (!backward) return pad256(4 * h);
+    if (!backward) return fused_f32(s) ? 0 : pad256(4 * h);
     return 2 * pad256(4 * h) + pad256(4 * x) +
-           kron_linear_workspace_size(s.N, s.p, s.q, s.m1, s.m2, s.r, KRON_F32);
+           2 * kron_linear_workspace_size(s.N, s.p, s.q, s.m1, s.m2, s.r, KRON_F32);
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -237,13 +221,17 @@ kron_status_t kron_glu_forward(const void *x, const void *S, const void *A, cons
         a.activation = activation;
         e = glu::tc_run(pl, a, glu::kForward, cs);
     } else {
-        e = pre_f32(x, S, A, B, bias, (float *)workspace, (float *)h, s, cs);
-        if (e == cudaSuccess) {
-            const int64_t n4 = N * s.d_out() / 4;
-            launch_step() = "gate launch";
-            gate_f32_kernel<<<grid_for(n4), 256, 0, cs>>>((const float4 *)workspace, (float4 *)h,
-                                                         n4, activation);
-            e = cudaGetLastError();
+        if (fused_f32(s)) {
+            e = glu::simt_pre(x, S, A, B, bias, nullptr, h, nullptr, s, activation, false, cs);
+        } else {
+            e = pre_f32(x, S, A, B, bias, (float *)workspace, (float *)h, s, cs);
+            if (e == cudaSuccess) {
+                const int64_t n4 = N * s.d_out() / 4;
+                launch_step() = "gate launch";
+                gate_f32_kernel<<<grid_for(n4), 256, 0, cs>>>(
+                    (const float4 *)workspace, (float4 *)h, n4, activation);
+                e = cudaGetLastError();
+            }
         }
     }
     return e == cudaSuccess ? KRON_OK : cuda_bad(e, "gated forward");
@@ -314,23 +302,23 @@ kron_status_t kron_glu_backward(const void *x, const void *S, const void *A, con
     float *part = (float *)(ws + 2 * hb + pad256((size_t)N * din * 4));
     const int parts = (int)(kron_linear_workspace_size(N, p, q, m1, m2, r, KRON_F32) /
                             (partial_stride(s) * sizeof(float)));
-    e = pre_f32(x, S, A, B, bias, g, u, s, cs);
-    if (e == cudaSuccess) {
-        const int64_t n4 = N * s.d_out() / 4;
-        launch_step() = "gate launch";
-        gate_grad_f32_kernel<<<grid_for(n4), 256, 0, cs>>>((float4 *)g, (float4 *)u,
-                                                          (const float4 *)dH, n4, activation);
-        e = cudaGetLastError();
+    if (fused_f32(s)) {
+        e = glu::simt_pre(x, S, A, B, bias, dH, g, u, s, activation, true, cs);
+    } else {
+        e = pre_f32(x, S, A, B, bias, g, u, s, cs);
+        if (e == cudaSuccess) {
+            const int64_t n4 = N * s.d_out() / 4;
+            launch_step() = "gate launch";
+            gate_grad_f32_kernel<<<grid_for(n4), 256, 0, cs>>>((float4 *)g, (float4 *)u,
+                                                              (const float4 *)dH, n4, activation);
+            e = cudaGetLastError();
+        }
     }
-    for (int k = 0; k < 2 && e == cudaSuccess; ++k) {
-        const Half f = half_of(S, A, B, nullptr, s, k);
-        e = simt_backward(x, f.S, f.A, f.B, k ? u : g, dX ? (k ? (void *)dx2 : dX) : nullptr, part,
-                          parts, s, false, cs);
-        if (e == cudaSuccess)
-            e = reduce_partials(part, parts, f.S, f.A, false, (float *)dS + k * pq,
-                                (float *)dA + k * r * pq, (float *)dB + k * r * mm,
-                                dbias ? (float *)dbias + k * dout : nullptr, s, 0.0, cs);
-    }
+    if (e == cudaSuccess)
+        e = glu::simt_backward_pair(x, S, A, B, g, u, dX, dX ? dx2 : nullptr, part, parts, s, cs);
+    if (e == cudaSuccess)
+        e = glu::reduce_partials_pair(part, parts, S, A, (float *)dS, (float *)dA, (float *)dB,
+                                      (float *)dbias, s, cs);
     if (e == cudaSuccess && dX) {
         const int64_t n4 = N * s.d_in() / 4;
         launch_step() = "dX launch";

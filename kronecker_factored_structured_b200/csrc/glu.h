@@ -36,6 +36,23 @@ struct Plan {
     int ntiles, groups;       // row tiles, and CTAs per slice
 };
 
+// ---- exact FP32 (simt_f32.cu) ----
+// Whether both projections, the activation and the product of this shape run as one kernel.
+bool simt_pre_supported(const Shape &s);
+// h (grad = false), or dg and du from dH (grad = true); factors stacked gate, up.
+cudaError_t simt_pre(const void *x, const void *S, const void *A, const void *B, const void *bias,
+                     const void *dH, void *out0, void *out1, const Shape &s, int activation,
+                     bool grad, cudaStream_t st);
+// simt_backward of both projections: gradients G0, G1 into dX0, dX1 (may be null) and the
+// partials of gate and up, parts x partial_stride floats each, into ws.
+cudaError_t simt_backward_pair(const void *x, const void *S, const void *A, const void *B,
+                               const void *G0, const void *G1, void *dX0, void *dX1, float *ws,
+                               int parts, const Shape &s, cudaStream_t st);
+// reduce_partials of both projections; gradients stacked as the factors are (reduce.cu).
+cudaError_t reduce_partials_pair(const float *ws, int parts, const void *S, const void *A,
+                                 float *dS, float *dA, float *dB, float *dbias, const Shape &s,
+                                 cudaStream_t st);
+
 bool tc_plan(Plan *pl, const Shape &s, Mode mode, int sms);
 
 struct TcArgs {
@@ -51,7 +68,7 @@ cudaError_t tc_run(const Plan &pl, const TcArgs &a, Mode mode, cudaStream_t st);
 // Dense weight gradients of the two projections, x^T [dg | du], in split row ranges, then
 // the factors' gradients from them.
 struct WgradPlan {
-    int splits;
+    int splits, tm;           // row ranges; rows of dW per tile
     int64_t rows_per_split;
     size_t part_floats;       // one split: [2][din][dout] and the column sums [2][dout]
     int dbs;                  // ranges of (a) that dB's partial sums are split into
@@ -61,6 +78,31 @@ WgradPlan wgrad_plan(const Shape &s, int sms);
 cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const void *du,
                       const void *S, const void *A, const void *B, void *dS, void *dA, void *dB,
                       void *dbias, void *ws, const Shape &s, cudaStream_t st);
+
+// act(g) and act'(g) with the accurate functions (exact-FP32 path).
+__device__ __forceinline__ float act_f32(int act, float g, float *d) {
+    if (act == KRON_ACT_GELU) {
+        const float c = 0.5f * erfcf(-g * 0.70710678118654752f);
+        const float e = expf(-0.5f * g * g);
+        *d = c + (e == 0.f ? 0.f : g * e * 0.39894228040143268f);
+        return g * c;
+    }
+    if (act == KRON_ACT_GELU_TANH) {
+        const float g2 = g * g;
+        const float v = 1.5957691216057308f * g * (1.f + 0.044715f * g2);
+        const float s = 1.f / (1.f + expf(-v)), w = s * (1.f / (1.f + expf(v)));
+        *d = s + (w == 0.f ? 0.f : g * w * 1.5957691216057308f * (1.f + 0.134145f * g2));
+        return g * s;
+    }
+    const float s = 1.f / (1.f + expf(-g)), c = 1.f / (1.f + expf(g));   // c = 1 - s
+    if (act == KRON_ACT_SIGMOID) {
+        *d = s * c;
+        return s;
+    }
+    const float f = g * s;
+    *d = s + f * c;
+    return f;
+}
 
 // Activation and derivative from hardware exponentials and reciprocals (about 2^-21 of the
 // value: far below the bfloat16 rounding of what is stored).

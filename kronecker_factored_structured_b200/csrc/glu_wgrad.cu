@@ -37,6 +37,7 @@ struct DwArgs {
     size_t part_floats;
     int64_t N, rows_per_split;
     int din, dout, mt, nt;       // tiles along din, and along dout of one projection
+    int tm;                      // rows of dW per tile: 256, or 128 where the tiles are few
     int sums;                    // whether the column sums are wanted
     int *device_error;
 };
@@ -57,13 +58,13 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
 
     const int tiles = g.mt * g.nt * 2;
     const int split = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-    const int m0 = (tile % g.mt) * kTM, proj = tile / (g.mt * g.nt);
+    const int m0 = (tile % g.mt) * g.tm, proj = tile / (g.mt * g.nt);
     const int n0 = (tile / g.mt) % g.nt * kTN;
     const int64_t r0 = split * g.rows_per_split;
     const int64_t r1 = min(g.N, r0 + g.rows_per_split);
     const int steps = (int)((r1 - r0 + kTK - 1) / kTK);
     const bool sums = g.sums && m0 == 0;
-    const bool second = m0 + 128 < g.din;      // whether the tile's lower half has rows of dW
+    const bool second = g.tm == kTM && m0 + 128 < g.din;      // whether the tile's lower half has rows of dW
     const int a_boxes = second ? 4 : 2;
 
     if (threadIdx.x == 0) {
@@ -167,13 +168,15 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         }
         done = warp_wait(bar(kDone), 0, ab);
         tc_fence_after();
-        if (done && (half == 0 || second)) {
-            const int row = m0 + half * 128 + quad * 32 + lane;
+        if (done) {
+            // the halves of the warps take the two accumulators, or every second column group
+            const int acc = second ? half : 0, step = second ? 1 : 2;
+            const int row = m0 + acc * 128 + quad * 32 + lane;
             float *dst = part + ((size_t)proj * g.din + row) * g.dout + n0;
-            for (int cg = 0; cg < kTN / 32; ++cg) {
+            for (int cg = second ? 0 : half; cg < kTN / 32; cg += step) {
                 if (n0 + cg * 32 >= g.dout) break;
                 uint32_t v[32];
-                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + half * 256 + cg * 32, v);
+                tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * 256 + cg * 32, v);
                 if (row < g.din) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
@@ -195,7 +198,7 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
 // dW is read as float4 along k, twice (second time from L2): once with a block per few (a, c)
 // for dC, once with a thread per four (j, k) for dB.
 constexpr int kCt = 256;      // threads
-constexpr int kRc = 8;        // ranks summed at a time
+constexpr int kW = 2;         // places of dW read at a time
 constexpr int kJs = 4;        // parts of j (dC)
 
 struct CtArgs {
@@ -210,21 +213,44 @@ struct CtArgs {
     int dc_blocks;               // blocks of the first role
 };
 
-__device__ __forceinline__ float4 dw4(const CtArgs &g, size_t o) {
-    float4 v = __ldg(reinterpret_cast<const float4 *>(g.part + o));
-    for (int s = 1; s < g.splits; ++s) {
-        const float4 w =
-            __ldg(reinterpret_cast<const float4 *>(g.part + (size_t)s * g.part_floats + o));
-        v.x += w.x;
-        v.y += w.y;
-        v.z += w.z;
-        v.w += w.w;
+// dW at W places, the splits added in order: 2 W loads in flight.
+template <int W>
+__device__ __forceinline__ void dw4(const CtArgs &g, const size_t (&o)[W], float4 (&v)[W]) {
+    auto add = [](float4 &x, const float4 &y) {
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+    };
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float *p = g.part;
+    int s = 0;
+    for (; s + 1 < g.splits; s += 2, p += 2 * g.part_floats) {
+        float4 x[W], y[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            x[i] = __ldg(reinterpret_cast<const float4 *>(p + o[i]));
+            y[i] = __ldg(reinterpret_cast<const float4 *>(p + g.part_floats + o[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            add(v[i], x[i]);
+            add(v[i], y[i]);
+        }
     }
-    return v;
+    if (s < g.splits) {
+        float4 x[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = __ldg(reinterpret_cast<const float4 *>(p + o[i]));
+#pragma unroll
+        for (int i = 0; i < W; ++i) add(v[i], x[i]);
+    }
 }
 
 // dC, dA, dS: a block per (projection, a, cpb columns c); a thread has four k of one c and a
 // quarter of the j, and the threads of one c are added in order.
+template <int kRc>   // ranks summed at a time
 __device__ void dc_role(const CtArgs &g) {
     __shared__ float acc_s[kRc][kCt];
     const int ncb = cdiv(g.q, g.cpb), blk = blockIdx.x;
@@ -241,19 +267,25 @@ __device__ void dc_role(const CtArgs &g) {
         float acc[kRc] = {};
         if (live) {
             const __nv_bfloat16 *Bi = g.B + ((size_t)proj * g.r + i0) * mm + 4 * kk;
-#pragma unroll 2
-            for (int j = j0; j < j1; ++j) {
-                const float4 v = dw4(g, o0 + (size_t)j * g.dout);
+            for (int j = j0; j < j1; j += kW) {
+                size_t o[kW];
+                float4 v[kW];
 #pragma unroll
-                for (int i = 0; i < kRc; ++i)
-                    if (i < ni) {
-                        const uint2 w = __ldg(
-                            reinterpret_cast<const uint2 *>(Bi + i * mm + (size_t)j * g.m2));
-                        acc[i] = fmaf(v.x, __uint_as_float(w.x << 16), acc[i]);
-                        acc[i] = fmaf(v.y, __uint_as_float(w.x & 0xFFFF0000u), acc[i]);
-                        acc[i] = fmaf(v.z, __uint_as_float(w.y << 16), acc[i]);
-                        acc[i] = fmaf(v.w, __uint_as_float(w.y & 0xFFFF0000u), acc[i]);
-                    }
+                for (int t = 0; t < kW; ++t) o[t] = o0 + (size_t)min(j + t, j1 - 1) * g.dout;
+                dw4(g, o, v);
+#pragma unroll
+                for (int t = 0; t < kW; ++t)
+                    if (j + t < j1)
+#pragma unroll
+                        for (int i = 0; i < kRc; ++i)
+                            if (i < ni) {
+                                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(
+                                    Bi + i * mm + (size_t)(j + t) * g.m2));
+                                acc[i] = fmaf(v[t].x, __uint_as_float(w.x << 16), acc[i]);
+                                acc[i] = fmaf(v[t].y, __uint_as_float(w.x & 0xFFFF0000u), acc[i]);
+                                acc[i] = fmaf(v[t].z, __uint_as_float(w.y << 16), acc[i]);
+                                acc[i] = fmaf(v[t].w, __uint_as_float(w.y & 0xFFFF0000u), acc[i]);
+                            }
             }
         }
         __syncthreads();
@@ -274,18 +306,24 @@ __device__ void dc_role(const CtArgs &g) {
             }
         }
         __syncthreads();
-        if (threadIdx.x < g.cpb && c0 + (int)threadIdx.x < g.q)
-            for (int i = 0; i < ni; ++i)
-                ds = fmaf(acc_s[i][threadIdx.x * g.tk],
-                          __bfloat162float(g.A[((size_t)proj * g.r + i0 + i) * pq +
-                                               (size_t)a * g.q + c0 + threadIdx.x]),
-                          ds);
+        if (threadIdx.x < g.cpb && c0 + (int)threadIdx.x < g.q) {
+            float af[kRc];
+#pragma unroll
+            for (int i = 0; i < kRc; ++i)
+                af[i] = i < ni ? __bfloat162float(g.A[((size_t)proj * g.r + i0 + i) * pq +
+                                                      (size_t)a * g.q + c0 + threadIdx.x])
+                               : 0.f;
+#pragma unroll
+            for (int i = 0; i < kRc; ++i)
+                if (i < ni) ds = fmaf(acc_s[i][threadIdx.x * g.tk], af[i], ds);
+        }
     }
     if (threadIdx.x < g.cpb && c0 + (int)threadIdx.x < g.q)
         g.dS[proj * pq + (size_t)a * g.q + c0 + threadIdx.x] = __float2bfloat16_rn(ds);
 }
 
 // dB partial sums: a thread per four (j, k), a block per (projection, range of (a, c), ranks)
+template <int kRc>
 __device__ void db_role(const CtArgs &g, int blk) {
     __shared__ float cs[kRc][64];      // C_i of up to 64 (a, c)
     const int n4 = g.m1 * g.tk, eb = cdiv(n4, kCt), ib = cdiv(g.r, kRc);
@@ -312,19 +350,27 @@ __device__ void db_role(const CtArgs &g, int blk) {
         __syncthreads();
         if (live) {
             int a = f / g.q, c = f - a * g.q;
-#pragma unroll 4
-            for (int w = 0; w < nf; ++w) {
-                const float4 v = dw4(g, (((size_t)proj * g.p + a) * g.m1 + j) * g.dout +
-                                            (size_t)c * g.m2 + k);
-                if (++c == g.q) c = 0, ++a;
+            const size_t o0 = ((size_t)proj * g.p * g.m1 + j) * g.dout + k;
+            for (int w = 0; w < nf; w += kW) {
+                size_t o[kW];
+                float4 v[kW];
 #pragma unroll
-                for (int i = 0; i < kRc; ++i) {
-                    const float x = cs[i][w];
-                    acc[i][0] = fmaf(v.x, x, acc[i][0]);
-                    acc[i][1] = fmaf(v.y, x, acc[i][1]);
-                    acc[i][2] = fmaf(v.z, x, acc[i][2]);
-                    acc[i][3] = fmaf(v.w, x, acc[i][3]);
+                for (int t = 0; t < kW; ++t) {
+                    o[t] = o0 + (size_t)a * g.m1 * g.dout + (size_t)c * g.m2;
+                    if (w + t + 1 < nf && ++c == g.q) c = 0, ++a;
                 }
+                dw4(g, o, v);
+#pragma unroll
+                for (int t = 0; t < kW; ++t)
+                    if (w + t < nf)
+#pragma unroll
+                        for (int i = 0; i < kRc; ++i) {
+                            const float x = cs[i][w + t];
+                            acc[i][0] = fmaf(v[t].x, x, acc[i][0]);
+                            acc[i][1] = fmaf(v[t].y, x, acc[i][1]);
+                            acc[i][2] = fmaf(v[t].z, x, acc[i][2]);
+                            acc[i][3] = fmaf(v[t].w, x, acc[i][3]);
+                        }
             }
         }
     }
@@ -338,24 +384,35 @@ __device__ void db_role(const CtArgs &g, int blk) {
                     make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
 }
 
-__global__ void __launch_bounds__(kCt) glu_contract_kernel(const CtArgs g) {
-    if ((int)blockIdx.x < g.dc_blocks) dc_role(g);
-    else db_role(g, blockIdx.x - g.dc_blocks);
+template <int kRc>
+__global__ void __launch_bounds__(kCt, 4) glu_contract_kernel(const CtArgs g) {
+    if ((int)blockIdx.x < g.dc_blocks) dc_role<kRc>(g);
+    else db_role<kRc>(g, blockIdx.x - g.dc_blocks);
 }
 
-// dB and dbias: the ranges and splits added in order.
+// dB and dbias: the ranges and splits, eight threads per value, each adding every eighth in
+// order, then their sums in order.
 __global__ void __launch_bounds__(kCt)
 glu_finish_kernel(const float *dbp, int dbs, size_t nb, __nv_bfloat16 *dB, const float *sums,
                   size_t part_floats, int splits, size_t nbias, __nv_bfloat16 *dbias) {
-    const size_t e = (size_t)blockIdx.x * kCt + threadIdx.x;
+    __shared__ float red[8][32];
+    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    const size_t e = (size_t)blockIdx.x * 32 + lane;
+    float v = 0.f;
     if (e < nb) {
-        float v = 0.f;
-        for (int s = 0; s < dbs; ++s) v += dbp[(size_t)s * nb + e];
-        dB[e] = __float2bfloat16_rn(v);
-    } else if (dbias && e - nb < nbias) {
-        float v = 0.f;
-        for (int s = 0; s < splits; ++s) v += sums[(size_t)s * part_floats + e - nb];
-        dbias[e - nb] = __float2bfloat16_rn(v);
+#pragma unroll 4
+        for (int s = part; s < dbs; s += 8) v += dbp[(size_t)s * nb + e];
+    } else if (e - nb < nbias) {
+        for (int s = part; s < splits; s += 8) v += sums[(size_t)s * part_floats + e - nb];
+    }
+    red[part][lane] = v;
+    __syncthreads();
+    if (part == 0 && e < nb + nbias) {
+        v = 0.f;
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v += red[t][lane];
+        if (e < nb) dB[e] = __float2bfloat16_rn(v);
+        else dbias[e - nb] = __float2bfloat16_rn(v);
     }
 }
 
@@ -363,23 +420,27 @@ size_t pad64(size_t n) { return (n + 63) & ~(size_t)63; }
 
 }  // namespace
 
+static int ranks_at_a_time(int r) { return r <= 4 ? 4 : 8; }
+
 WgradPlan wgrad_plan(const Shape &s, int sms) {
     WgradPlan pl{};
     const int din = (int)s.d_in(), dout = (int)s.d_out();
     const int64_t tiles = (int64_t)cdiv(din, kTM) * 2 * cdiv(dout, kTN);
     int64_t splits = sms / tiles;
-    const int64_t most = (s.N + 255) / 256;    // at least four stages of rows per range
+    // a range costs a write and two reads of dW: at least 16 stages of rows for it
+    const int64_t most = (s.N + 1023) / 1024;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
     pl.rows_per_split = ((s.N + splits - 1) / splits + kTK - 1) / kTK * kTK;
     if (pl.rows_per_split < kTK) pl.rows_per_split = kTK;
     pl.splits = (int)((s.N + pl.rows_per_split - 1) / pl.rows_per_split);
     if (pl.splits < 1) pl.splits = 1;
+    pl.tm = 2 * tiles * pl.splits <= sms ? 128 : kTM;
     pl.part_floats = pad64((size_t)2 * din * dout + 2 * (size_t)dout);
-    // dB: ranges of (a, c) for about two blocks per SM, at most 64 (their sums are added again)
-    const int64_t per = (int64_t)cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, kRc) * 2;
-    int64_t dbs = (2 * sms + per - 1) / per;
-    if (dbs > 64) dbs = 64;
+    // dB: ranges of (a, c) for about four blocks per SM, at most 128 (their sums are added again)
+    const int64_t per = (int64_t)cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, ranks_at_a_time(s.r)) * 2;
+    int64_t dbs = (4 * sms + per - 1) / per;
+    if (dbs > 128) dbs = 128;
     if (dbs > (int64_t)s.p * s.q) dbs = (int64_t)s.p * s.q;
     pl.dbs = (int)dbs;
     pl.ws_bytes = 4 * (pl.part_floats * pl.splits +
@@ -404,7 +465,8 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
     g.rows_per_split = pl.rows_per_split;
     g.din = din;
     g.dout = dout;
-    g.mt = cdiv(din, kTM);
+    g.tm = pl.tm;
+    g.mt = cdiv(din, pl.tm);
     g.nt = cdiv(dout, kTN);
     g.sums = dbias != nullptr;
     launch_step() = "device error word";
@@ -441,14 +503,17 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
     if (c.cpb < 1) return cudaErrorInvalidValue;       // m2 <= 256: checked by the entry points
     if (c.cpb > s.q) c.cpb = s.q;
     c.dc_blocks = 2 * s.p * cdiv(s.q, c.cpb);
-    const int db_blocks = cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, kRc) * pl.dbs * 2;
+    const int db_blocks = cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, ranks_at_a_time(s.r)) * pl.dbs * 2;
     launch_step() = "factor-gradient launch";
-    glu_contract_kernel<<<(unsigned)(c.dc_blocks + db_blocks), kCt, 0, st>>>(c);
+    if (ranks_at_a_time(s.r) == 4)
+        glu_contract_kernel<4><<<(unsigned)(c.dc_blocks + db_blocks), kCt, 0, st>>>(c);
+    else
+        glu_contract_kernel<8><<<(unsigned)(c.dc_blocks + db_blocks), kCt, 0, st>>>(c);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const size_t nb = (size_t)2 * s.r * s.m1 * s.m2, nbias = dbias ? (size_t)2 * dout : 0;
     launch_step() = "final sums launch";
-    glu_finish_kernel<<<(unsigned)((nb + nbias + kCt - 1) / kCt), kCt, 0, st>>>(
+    glu_finish_kernel<<<(unsigned)((nb + nbias + 31) / 32), kCt, 0, st>>>(
         c.dbp, pl.dbs, nb, static_cast<__nv_bfloat16 *>(dB),
         g.part + (size_t)2 * din * dout, pl.part_floats, pl.splits, nbias,
         static_cast<__nv_bfloat16 *>(dbias));

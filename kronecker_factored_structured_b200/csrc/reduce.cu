@@ -13,6 +13,7 @@
 // independent accumulators, which are then added in a fixed order.  The order depends only
 // on `parts`, so results are bitwise reproducible.  Many warps per column keep each
 // thread's chain of dependent loads short: the kernel is latency-bound, not byte-bound.
+#include "glu.h"
 #include "internal.h"
 
 #include <cuda_bf16.h>
@@ -82,6 +83,15 @@ kron_reduce_kernel(const float *__restrict__ ws, int parts, size_t stride,
     const size_t pq = (size_t)s.p * s.q;
     const size_t n_dc = (size_t)s.r * pq, n_db = (size_t)s.r * s.m1 * s.m2;
     const size_t n_b = (size_t)s.q * s.m2;
+    if (blockIdx.y) {      // the second projection of a stacked pair
+        ws += (size_t)parts * stride;
+        S += pq;
+        A += n_dc;
+        dS += pq;
+        dA += n_dc;
+        dB += n_db;
+        dbias += dbias ? n_b : 0;
+    }
     const int lane = threadIdx.x;
     int blk = blockIdx.x;
     if (blk < blocks_dc) {
@@ -129,6 +139,22 @@ kron_reduce_kernel(const float *__restrict__ ws, int parts, size_t stride,
 }
 
 }  // namespace
+
+namespace glu {
+cudaError_t reduce_partials_pair(const float *ws, int parts, const void *S, const void *A,
+                                 float *dS, float *dA, float *dB, float *dbias, const Shape &s,
+                                 cudaStream_t st) {
+    const int blocks_dc = (int)(((size_t)s.p * s.q + 31) / 32);
+    const int blocks_db = (int)(((size_t)s.r * s.m1 * s.m2 + 31) / 32);
+    const int blocks_b = dbias ? (int)(((size_t)s.q * s.m2 + 31) / 32) : 0;
+    launch_step() = "reduction launch";
+    kron_reduce_kernel<float>
+        <<<dim3((unsigned)(blocks_dc + blocks_db + blocks_b), 2), dim3(32, kWarps), 0, st>>>(
+            ws, parts, partial_stride(s), (const float *)S, (const float *)A, dS, dA, dB, dbias, s,
+            blocks_dc, blocks_db, 0.0);
+    return cudaGetLastError();
+}
+}  // namespace glu
 
 cudaError_t reduce_partials(const float *ws, int parts, const void *S, const void *A,
                             bool is_bf16, float *dS, float *dA, float *dB, float *dbias,

@@ -85,7 +85,7 @@ def test_bf16_rows(N, name):
     compare(run(d, name, "bf16"), reference(d, name), "bf16")
 
 
-F32 = [(4, 4, 4, 4, 1, 3), (9, 11, 12, 20, 3, 37), (32, 32, 32, 32, 4, 65), (1, 1, 4, 4, 1, 1),
+F32 = [(32, 32, 32, 32, 4, 2500), (128, 128, 8, 8, 2, 19), (64, 64, 64, 64, 2, 5), (4, 4, 4, 4, 1, 3), (9, 11, 12, 20, 3, 37), (32, 32, 32, 32, 4, 65), (1, 1, 4, 4, 1, 1),
        (32, 24, 16, 32, 2, 777), (7, 3, 28, 8, 2, 150)]
 
 

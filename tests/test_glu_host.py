@@ -48,8 +48,12 @@ def test_backward_rejects(dtype, kwargs, status):
 
 
 def test_forward_f32_wants_its_workspace():
-    assert call(False, dtype=0, ws=None) == 4
-    assert call(False, dtype=0, ws=V(0x10010)) == 3
+    """The compiled shape over many rows goes through one pre-activation in memory."""
+    big = dict(dtype=0, N=4096, p=32, q=32, m1=32, m2=32, r=4)
+    assert native.glu_workspace_size(4096, 32, 32, 32, 32, 4, "f32") == 4096 * 1024 * 4
+    assert call(False, ws=None, **big) == 4
+    assert call(False, ws_bytes=4096, **big) == 4
+    assert call(False, ws=V(0x10010), **big) == 3
 
 
 def test_empty_forward_is_fine():
@@ -59,7 +63,7 @@ def test_empty_forward_is_fine():
 def test_workspace_size():
     size = native.glu_workspace_size
     assert size(100, 4, 4, 16, 16, 2, "bf16") == 0            # the forward needs none
-    assert size(100, 4, 4, 16, 16, 2, "f32") == 100 * 64 * 4
+    assert size(100, 4, 4, 16, 16, 2, "f32") == 0             # one kernel
     for dt in ("f32", "bf16"):
         n = size(100, 4, 4, 16, 16, 2, dt, True)
         assert n > 0 and n == size(100, 4, 4, 16, 16, 2, dt, True)
