@@ -25,7 +25,6 @@ struct Plan {
     int nac, AC;              // chunks of the a index, and their width
     int nblk, nblk_src;       // rank blocks in all and per source
     int sw, kch, kb;          // x rows: swizzle width, chunks of it per row, bytes per row
-    int nacc;                 // accumulators (gate and up, or their sum)
     int nqs, qc, qcp, nks;    // c slices, columns per slice (and padded to 16), k slices
     int ybufs, stages, tbufs, dbufs;   // buffers of Y, x, T and D1
     int g1;                            // groups of epilogue-1 warps at work

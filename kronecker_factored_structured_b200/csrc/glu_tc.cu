@@ -13,8 +13,8 @@
 // accumulator and those of up ranks to another, so that x is read once for both.  Epilogue 1
 // (12 warps) moves a chunk TMEM -> bf16 -> shared memory, which is the permute of the vec trick;
 // epilogue 2 (16 warps) has g and u of one (n, k, c) side by side.  For kInput the kernel runs
-// with transposed factors, dg against the gate's and du against the up's ranks, all into one
-// accumulator.  T is rounded to BF16 between the stages, as in the layer's own kernels: half
+// with transposed factors, dg against the gate's and du against the up's ranks, and the two
+// accumulators are added.  T is rounded to BF16 between the stages, as in the layer's own kernels: half
 // a step, 2^-8 of each term.
 //
 // A CTA holds the factors of one (k slice, c slice) in shared memory for its life and streams
@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kE1 = 12, kE2 = 16;      // epilogue warps
 constexpr int kG1 = kE1 / 4;           // groups of epilogue-1 warps, one chunk each at a time
-constexpr int kThreads = 32 * (3 + kE1 + kE2);   // and TMA and two MMA issuers
+constexpr int kThreads = 32 * (4 + kE1 + kE2);   // and TMA and three MMA issuers
 constexpr int kMaxStages = 6;
 constexpr int kTailBytes = 512;        // barriers, TMEM address, abort flag
 constexpr int kSmemMax = 232448 - 1024 - kTailBytes;
@@ -61,7 +61,7 @@ struct KArgs {
 // Barriers, in 8-byte words from the tail's start.
 enum { kXFull = 0, kXEmpty = kMaxStages, kD1Full = 2 * kMaxStages, kD1Empty = kD1Full + kMaxD,
        kTFull = kD1Empty + kMaxD, kTEmpty = kTFull + kMaxT, kYFull = kTEmpty + kMaxT,
-       kYEmpty = kYFull + 2, kDrain = kYEmpty + 2, kBars = kDrain + 2 };
+       kYEmpty = kYFull + 2, kDrain = kYEmpty + 2, kBars = kDrain + 3 };
 static_assert(kBars * 8 + 16 <= kTailBytes, "tail");
 
 // A shared-memory descriptor from its low word (address) and the high word of its layout: steps
@@ -105,17 +105,8 @@ __device__ __forceinline__ void gate_pairs(int act, const float (&g)[8], const f
 #undef KRON_GATE
 }
 
-// 16 lanes x 16 columns in the 16x256b pattern (tmem_load16x256_x4 with two repetitions) of
-// one or two accumulators, one wait for both.
-__device__ __forceinline__ void tmem_load16x256_x2(uint32_t ta, uint32_t (&r)[8]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7])
-        : "r"(ta)
-        : "memory");
-}
+// 16 lanes x 16 columns in the 16x256b pattern (tmem_load16x256_x4 with two repetitions) of two
+// accumulators, one wait for both.
 __device__ __forceinline__ void tmem_load16x256_x2(uint32_t ta, uint32_t tb, uint32_t (&r)[8],
                                                    uint32_t (&q)[8]) {
     asm volatile(
@@ -157,7 +148,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
     constexpr bool TR = MODE == kInput;
     const int x_chunks = pl.nsrc * pl.nac;     // ring items of a tile
 
-    // x chunk (source, ac) of tile t into ring slot s, by one thread
+    // x chunk (ac, source) of tile t into ring slot s, by one thread
     auto issue_x = [&](int t, int ac, int src, int s) {
         const CUtensorMap *map = src ? &map1 : &map0;
         mbar_arrive_expect_tx(bar(kXFull + s), N1 * pl.kb);
@@ -172,9 +163,9 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
     // the producer's position: ring slot and parity, tile, chunk (warp 0 lane 0)
     int xs = 0, xph = 1, xt = group, xac = 0, xsrc = 0, xissued = 0;
     auto advance_x = [&]() {
-        if (++xac == pl.nac) {
-            xac = 0;
-            if (++xsrc == pl.nsrc) xsrc = 0, xt += pl.groups;
+        if (++xsrc == pl.nsrc) {
+            xsrc = 0;
+            if (++xac == pl.nac) xac = 0, xt += pl.groups;
         }
         if (++xs == pl.stages) xs = 0, xph ^= 1;
         ++xissued;
@@ -191,13 +182,14 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
         }
         for (int d = 0; d < kMaxT; ++d) {
             mbar_init(bar(kTFull + d), 4);
-            mbar_init(bar(kTEmpty + d), 1);
+            mbar_init(bar(kTEmpty + d), 2);
         }
         for (int d = 0; d < 2; ++d) {
-            mbar_init(bar(kYFull + d), 1);
+            mbar_init(bar(kYFull + d), 2);
             mbar_init(bar(kYEmpty + d), kE2);
             mbar_init(bar(kDrain + d), 1);
         }
+        mbar_init(bar(kDrain + 2), 1);
         *ab.flag = 0;
         mbar_init_fence();
         prefetch_tmap(&map0);
@@ -265,7 +257,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                 }
             }
         }
-        // stage-2 B operand of chunk ch = (source, ac, block), in the order of the tile's
+        // stage-2 B operand of chunk ch = (ac, source, block), in the order of the tile's
         // chunks: row c, K position il*AC + a % AC: C_i[a][c0 + c]
         {
             const int cmax = min(pl.qc, pl.Q - c0);
@@ -304,7 +296,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                 place(f, so, bs, il);
                 const int a = TR ? in8 : row, ac = a / pl.AC;
                 const uint32_t kb = (uint32_t)(il * pl.AC + a - ac * pl.AC) * 2u;
-                const uint32_t at = sC + ((so * pl.nac + ac) * pl.nblk_src + bs) * pl.c_chunk +
+                const uint32_t at = sC + ((ac * pl.nsrc + so) * pl.nblk_src + bs) * pl.c_chunk +
                                     (kb >> 7) * (uint32_t)pl.qcp * 128u;
                 const uint32_t in = kb & 127u;
                 if constexpr (TR) {      // zeros behind p: inside the chunk's padding
@@ -374,7 +366,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                     break;
                 }
                 const uint32_t bd0 = x_lo + s * x_stage;
-                uint32_t ad0 = b_lo + (xc < pl.nac ? 0u : pl.nblk_src * a_blk);
+                uint32_t ad0 = b_lo + (TR && (xc & 1) ? pl.nblk_src * a_blk : 0u);
                 for (int b = 0; b < pl.nblk_src; ++b, ad0 += a_blk) {
                     if (!warp_wait(bar(kD1Empty + d1), dph, ab)) {
                         ok = false;
@@ -407,8 +399,13 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) mbar_wait_drain(bar(kDrain + 0), 0);
         __syncwarp();
-    } else if (warp == 2) {
-        // ---------------- stage 2 ----------------
+    } else if (warp < 4) {
+        // ---------------- stage 2: one warp per accumulator ----------------
+        // Gate's ranks (kInput: dg) and up's (du) go to accumulators of their own, each issued by
+        // one warp, so that one's waits and descriptors overlap the other's MMAs.  Both follow
+        // every chunk (an arrival in place of the MMAs of the other's), so that neither falls a
+        // phase behind.
+        const int me = warp - 2;
         const uint32_t idesc = idesc_f32acc(128, pl.qcp, 1);
         const uint64_t adt = sdesc_kmajor(sT, 128);
         const uint32_t hi = (uint32_t)(adt >> 32), t_lo = (uint32_t)adt;
@@ -416,95 +413,88 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
         const uint32_t t_buf = (uint32_t)pl.t_bytes >> 4, c_step = (uint32_t)pl.c_chunk >> 4;
         const uint32_t c_ch = 8u * pl.qcp;
         const int a16 = pl.AC >> 3;              // half K steps per rank
-        // blocks of gate ranks alone, and whether the next one holds both (kInput: no gate)
-        const int gate_blocks = MODE == kInput ? pl.nblk_src : pl.r / RB;
-        const bool mixed = MODE != kInput && pl.r % RB != 0;
         const int steps_full = (RB * a16) >> 1;
         const int steps_last = ((pl.ranks - (pl.nblk_src - 1) * RB) * a16) >> 1;
-        const int split = ((pl.r % RB) * a16) >> 1;   // K steps of the mixed block's gate ranks
+        // K steps [lo, hi) of a block are this warp's: with gate and up in one list, blocks below
+        // r / RB are gate's, the one at it may be both, the rest up's
+        const int edge = pl.r / RB, split = ((pl.r % RB) * a16) >> 1;
         int tb = 0, tph = 0, y = 0, yph = 1;
         bool ok = true;
         for (int t = group; t < pl.ntiles && ok; t += pl.groups) {
             if (!warp_wait(bar(kYEmpty + y), yph, ab)) break;
-            const uint32_t yb = tmem + pl.tm_y + y * pl.nacc * pl.qcp;
-            uint32_t acc0 = 0, acc1 = 0;      // whether an accumulator holds something
+            const uint32_t dst = tmem + pl.tm_y + (2 * y + me) * pl.qcp;
+            uint32_t acc = 0;                    // whether the accumulator holds something
             uint32_t bd0 = c_lo;
-            for (int ch = 0, bs = 0; ch < nchunks; ++ch, bd0 += c_step) {
+            for (int ch = 0, bs = 0, src = 0; ch < nchunks; ++ch, bd0 += c_step) {
+                const int steps = bs == pl.nblk_src - 1 ? steps_last : steps_full;
+                int k_lo = 0, k_hi = steps;
+                if (TR) {
+                    if (src != me) k_hi = 0;
+                } else if (me == 0) {
+                    if (bs >= edge) k_hi = bs == edge ? split : 0;
+                } else {
+                    if (bs <= edge) k_lo = bs == edge ? split : steps;
+                }
+                const uint32_t ad0 = t_lo + tb * t_buf;
                 if (!warp_wait(bar(kTFull + tb), tph, ab)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                const uint32_t ad0 = t_lo + tb * t_buf;
-                const int steps = bs == pl.nblk_src - 1 ? steps_last : steps_full;
-                const bool last = ch == nchunks - 1;
-                if (!(mixed && bs == gate_blocks)) {
-                    const bool up = MODE != kInput && bs >= gate_blocks;
-                    const uint32_t dst = up ? yb + pl.qcp : yb;
-                    const uint32_t acc = up ? acc1 : acc0;
-                    if (up) acc1 = 1;
-                    else acc0 = 1;
+                if (k_lo < k_hi) {
+                    tc_fence_after();
                     if (elect_one()) {
-                        mma_ss<false>(dst, desc_of(ad0, hi), desc_of(bd0, hi), idesc, acc);
-                        if (steps == 8) {
+                        if (k_hi - k_lo == 8) {
+                            mma_ss<false>(dst, desc_of(ad0, hi), desc_of(bd0, hi), idesc, acc);
 #pragma unroll
                             for (int ks = 1; ks < 8; ++ks)
                                 mma_ss<false>(
                                     dst, desc_of(ad0 + (ks >> 2) * 1024 + (ks & 3) * 2, hi),
                                     desc_of(bd0 + (ks >> 2) * c_ch + (ks & 3) * 2, hi), idesc, 1);
                         } else {
-                            for (int ks = 1; ks < steps; ++ks)
+                            for (int ks = k_lo; ks < k_hi; ++ks)
                                 mma_ss<false>(
                                     dst, desc_of(ad0 + (ks >> 2) * 1024 + (ks & 3) * 2, hi),
-                                    desc_of(bd0 + (ks >> 2) * c_ch + (ks & 3) * 2, hi), idesc, 1);
+                                    desc_of(bd0 + (ks >> 2) * c_ch + (ks & 3) * 2, hi), idesc,
+                                    acc | (uint32_t)(ks > k_lo));
                         }
                         mma_commit(bar(kTEmpty + tb));
-                        if (last) mma_commit(bar(kYFull + y));
                     }
-                } else {
-                    if (elect_one()) {
-                        for (int ks = 0; ks < steps; ++ks) {
-                            const bool up = ks >= split;
-                            mma_ss<false>(up ? yb + pl.qcp : yb,
-                                          desc_of(ad0 + (ks >> 2) * 1024 + (ks & 3) * 2, hi),
-                                          desc_of(bd0 + (ks >> 2) * c_ch + (ks & 3) * 2, hi),
-                                          idesc,
-                                          up ? (acc1 | (uint32_t)(ks > split))
-                                             : (acc0 | (uint32_t)(ks > 0)));
-                        }
-                        mma_commit(bar(kTEmpty + tb));
-                        if (last) mma_commit(bar(kYFull + y));
-                    }
-                    acc0 = acc1 = 1;
+                    acc = 1;
+                } else if (elect_one()) {
+                    mbar_arrive(bar(kTEmpty + tb));
                 }
                 __syncwarp();
                 if (++tb == pl.tbufs) tb = 0, tph ^= 1;
-                if (++bs == pl.nblk_src) bs = 0;
+                if (++bs == pl.nblk_src) {
+                    bs = 0;
+                    if (TR) src ^= 1;
+                }
             }
+            if (!ok) break;
+            if (elect_one()) mma_commit(bar(kYFull + y));
+            __syncwarp();
             if (++y == pl.ybufs) y = 0, yph ^= 1;
         }
-        if (elect_one()) mma_commit(bar(kDrain + 1));
+        if (elect_one()) mma_commit(bar(kDrain + 1 + me));
         __syncwarp();
-        if (lane == 0) mbar_wait_drain(bar(kDrain + 1), 0);
+        if (lane == 0) mbar_wait_drain(bar(kDrain + 1 + me), 0);
         __syncwarp();
-    } else if (warp < 3 + kE1) {
+    } else if (warp < 4 + kE1) {
         // ---------------- epilogue 1: D1 -> T ----------------
         // Groups of four warps, one per lane quadrant, take the chunks in turn: a chunk's loads,
         // conversions and stores take longer than its MMAs, and up to three are in flight.  No
         // more groups than buffers of D1 and of T: a group that waits for a buffer has then
         // seen the use before the last one end (it ended before the group's own last chunk was
         // stored), so the parity it waits for cannot be an older phase's.
-        const int quad = warp & 3, mine = (warp - 3) >> 2;
+        const int quad = warp & 3, mine = (warp - 4) >> 2;
         const int L = quad * 32 + lane, il = L / MP, l = L % MP;
         const uint32_t d1_addr = tmem + ((uint32_t)(quad * 32) << 16);
-        // byte offsets in T of this lane's stores: columns (n, a..a+7) go to row (n, l), K
-        // position il*AC + a
-        uint32_t soff[16];
+        // columns (n, a..a+7) of this lane go to row (n, l) of T, K position il*AC + a; with AC =
+        // MP that is one of MP/8 addresses and a constant (the swizzle depends on l alone)
+        const bool full = pl.AC == MP;
+        uint32_t soff[MP / 8];
 #pragma unroll
-        for (int t = 0; t < 16; ++t) {
-            const int f = t * 8, n = f / pl.AC, a = f % pl.AC;
-            soff[t] = f < N1 ? sT + kmaj(n * MP + l, (il * pl.AC + a) * 2, 128, 128) : 0xFFFFFFFFu;
-        }
+        for (int j = 0; j < MP / 8; ++j) soff[j] = sT + kmaj(l, (il * MP + j * 8) * 2, 128, 128);
         int d = mine, dph = 0, tb = mine, tph = 1, t = group, bs = mine, ch = mine;
         auto wrap = [&]() {
             while (d >= pl.dbufs) d -= pl.dbufs, dph ^= 1;
@@ -521,16 +511,37 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             const bool live = bs * RB + il < pl.ranks;
             const bool some = __any_sync(0xffffffffu, live);
             const uint32_t to = tb * pl.t_bytes;
+            if (some && full) {
+                // AC = MP: column group f lies in row n = f / MP, at a = f % MP
+                uint32_t base8[MP / 8];
 #pragma unroll
-            for (int gi = 0; gi < 4; ++gi) {
-                if (some && gi * 32 < N1) {
+                for (int j = 0; j < MP / 8; ++j) base8[j] = soff[j] + to;
+#pragma unroll
+                for (int gi = 0; gi < 4; ++gi) {
                     uint32_t r[32];
                     tmem_load32(d1_addr + d * 128 + gi * 32, r);
                     if (live) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (soff[gi * 4 + q] != 0xFFFFFFFFu)
-                                st_op16<__nv_bfloat16>(soff[gi * 4 + q] + to, &r[q * 8]);
+                        for (int q = 0; q < 4; ++q) {
+                            const int f = gi * 32 + q * 8;
+                            st_op16<__nv_bfloat16>(base8[f % MP / 8] + f / MP * MP * 128, &r[q * 8]);
+                        }
+                    }
+                }
+            } else if (some) {
+#pragma unroll 1
+                for (int gi = 0; gi * 32 < N1; ++gi) {
+                    uint32_t r[32];
+                    tmem_load32(d1_addr + d * 128 + gi * 32, r);
+                    if (live) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int f = gi * 32 + q * 8, n = f / pl.AC, a = f - n * pl.AC;
+                            if (f < N1)
+                                st_op16<__nv_bfloat16>(
+                                    sT + to + kmaj(n * MP + l, (il * pl.AC + a) * 2, 128, 128),
+                                    &r[q * 8]);
+                        }
                     }
                 }
             }
@@ -553,31 +564,39 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
         // (tile, group).  A thread holds, for the columns c = 2 tq, 2 tq + 1, + 8 and + 9 of the
         // group, the pair of values k, k + 1.  For kPre the dH of an item are fetched two items
         // ahead.
-        const int quad = warp & 3, wi = (warp - 3 - kE1) >> 2, w0c = wi >> 1;
+        const int quad = warp & 3, wi = (warp - 4 - kE1) >> 2, w0c = wi >> 1;
         const int L16 = quad * 32 + (wi & 1) * 16, n_l = L16 / MP;
         const int kl = L16 % MP + 2 * (lane >> 2), k = k0 + kl, tq = lane & 3;
         const uint32_t y_addr = tmem + ((uint32_t)L16 << 16) + pl.tm_y;
         const bool k_ok = k < pl.M2;
         const int ni = ((pl.qcp >> 4) + 1 - w0c) >> 1;     // items per tile
         const int qmax = min(pl.qc, pl.Q - c0) - 2 * tq;   // columns of this slice, from 2 tq on
-        const size_t lane_off = (size_t)n_l * g.out_ld + (size_t)(c0 + 2 * tq) * pl.M2 + k;
-        const uint32_t bias_addr = sBias + 2 * tq * kBiasRow + 8 * kl;
-        const size_t tile_step = (size_t)NT * g.out_ld;
+        const size_t lane_off =
+            (size_t)n_l * g.out_ld + (size_t)(c0 + 2 * tq + 16 * w0c) * pl.M2 + k;
+        const uint32_t bias_addr = sBias + (2 * tq + 16 * w0c) * kBiasRow + 8 * kl;
+        const size_t tile_step = (size_t)NT * g.out_ld * pl.groups;   // to this CTA's next tile
+        const size_t item_step = (size_t)32 * pl.M2;
+        const int nlast = (int)g.N - n_l;                   // rows t NT below it exist
         uint32_t dh[2][4] = {};
         int ft = group, fi = 0;                        // next item to fetch
+        const __nv_bfloat16 *fsrc =
+            MODE == kPre ? g.dH + (size_t)group * NT * g.out_ld + lane_off : nullptr;
         auto fetch_next = [&](uint32_t (&to)[4]) {
-            if (ft >= pl.ntiles || ni == 0) return;
-            const bool row_ok = (int64_t)ft * NT + n_l < g.N && k_ok;
-            const __nv_bfloat16 *src =
-                g.dH + (size_t)ft * tile_step + lane_off + (size_t)((w0c + 2 * fi) * 16) * pl.M2;
+            if (ft >= pl.ntiles) return;
+            const bool row_ok = ft * NT < nlast && k_ok;
+            const __nv_bfloat16 *src = fsrc + (size_t)fi * item_step;
+            const int left = row_ok ? qmax - (w0c + 2 * fi) * 16 : 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int c = (i & 1) + 8 * (i >> 1);
-                to[i] = row_ok && (w0c + 2 * fi) * 16 + c < qmax
-                            ? __ldg(reinterpret_cast<const unsigned int *>(src + c * pl.M2)) : 0u;
+                to[i] = c < left ? __ldg(reinterpret_cast<const unsigned int *>(src + c * pl.M2))
+                                 : 0u;
             }
-            if (++fi == ni) fi = 0, ft += pl.groups;
+            if (++fi == ni) fi = 0, ft += pl.groups, fsrc += tile_step;
         };
+        __nv_bfloat16 *p0 = g.out0 + (size_t)group * NT * g.out_ld + lane_off;
+        __nv_bfloat16 *p1 =
+            MODE == kPre ? g.out1 + (size_t)group * NT * g.out_ld + lane_off : nullptr;
         int t = group, item = 0, y = 0, yph = 0;
         // one item; false when the pipeline gave up
         auto process = [&](uint32_t (&d)[4]) -> bool {
@@ -586,17 +605,18 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                 tc_fence_after();
             }
             const int cb = (w0c + 2 * item) * 16;
-            const uint32_t ya = y_addr + y * pl.nacc * pl.qcp + cb;
+            const uint32_t ya = y_addr + 2 * y * pl.qcp + cb;
             uint32_t w0[4], w1[4];
             // registers 4 rep + (0, 1) hold k at the columns 8 rep + 2 tq (+ 1), 4 rep + (2, 3)
             // hold k + 1
             if constexpr (MODE == kInput) {
-                uint32_t r[8];
-                tmem_load16x256_x2(ya, r);
+                uint32_t r[8], q[8];
+                tmem_load16x256_x2(ya, ya + pl.qcp, r, q);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int o = 4 * (i >> 1) + (i & 1);
-                    w0[i] = pack_bf16x2(__uint_as_float(r[o]), __uint_as_float(r[o + 2]));
+                    w0[i] = pack_bf16x2(__uint_as_float(r[o]) + __uint_as_float(q[o]),
+                                        __uint_as_float(r[o + 2]) + __uint_as_float(q[o + 2]));
                 }
             } else {
                 uint32_t r[8], q[8];
@@ -613,7 +633,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                         const int c = (i & 1) + 8 * (i >> 1);
                         uint32_t v[4] = {0, 0, 0, 0};
                         if (pl.bias_smem) {
-                            ld_shared_v4(bias_addr + (cb + c) * kBiasRow, v);
+                            ld_shared_v4(bias_addr + (32 * item + c) * kBiasRow, v);
                         } else if (k_ok && cb + c < qmax) {
                             const __nv_bfloat16 *p =
                                 g.bias + (size_t)(c0 + 2 * tq + cb + c) * pl.M2 + k;
@@ -637,17 +657,26 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                 tc_fence_before();
                 mbar_arrive_warp(bar(kYEmpty + y));
             }
-            if ((int64_t)t * NT + n_l < g.N && k_ok) {
-                const size_t o = (size_t)t * tile_step + lane_off + (size_t)cb * pl.M2;
-                __nv_bfloat16 *p0 = g.out0 + o, *p1 = MODE == kPre ? g.out1 + o : nullptr;
+            if (t * NT < nlast && k_ok) {
+                const size_t o = (size_t)item * item_step;
                 const int left = qmax - cb;
+                if (left >= 10) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int c = (i & 1) + 8 * (i >> 1);
-                    if (c < left) {
-                        *reinterpret_cast<uint32_t *>(p0 + c * pl.M2) = w0[i];
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = (i & 1) + 8 * (i >> 1);
+                        *reinterpret_cast<uint32_t *>(p0 + o + c * pl.M2) = w0[i];
                         if constexpr (MODE == kPre)
-                            *reinterpret_cast<uint32_t *>(p1 + c * pl.M2) = w1[i];
+                            *reinterpret_cast<uint32_t *>(p1 + o + c * pl.M2) = w1[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = (i & 1) + 8 * (i >> 1);
+                        if (c < left) {
+                            *reinterpret_cast<uint32_t *>(p0 + o + c * pl.M2) = w0[i];
+                            if constexpr (MODE == kPre)
+                                *reinterpret_cast<uint32_t *>(p1 + o + c * pl.M2) = w1[i];
+                        }
                     }
                 }
             }
@@ -655,11 +684,13 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             if (++item == ni) {
                 item = 0;
                 t += pl.groups;
+                p0 += tile_step;
+                if constexpr (MODE == kPre) p1 += tile_step;
                 if (++y == pl.ybufs) y = 0, yph ^= 1;
             }
             return true;
         };
-        if constexpr (MODE == kPre) {
+        if (MODE == kPre && ni > 0) {
             fetch_next(dh[0]);
             fetch_next(dh[1]);
         }
@@ -671,10 +702,12 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             }
         while (t < pl.ntiles && ni > 0) {
             if (!process(dh[0])) break;
-            if constexpr (MODE == kPre) fetch_next(dh[0]);
-            if (t >= pl.ntiles) break;
-            if (!process(dh[1])) break;
-            if constexpr (MODE == kPre) fetch_next(dh[1]);
+            if constexpr (MODE == kPre) {
+                fetch_next(dh[0]);
+                if (t >= pl.ntiles) break;
+                if (!process(dh[1])) break;
+                fetch_next(dh[1]);
+            }
         }
     }
     tc_fence_before();
@@ -730,7 +763,6 @@ static bool find_plan(Plan *best, const Shape &s, Mode mode, int sms) {
         p.r = s.r;
         p.nsrc = tr ? 2 : 1;
         p.ranks = tr ? s.r : 2 * s.r;
-        p.nacc = tr ? 1 : 2;
         if (MP > 16 && MP >= 2 * p.M2) continue;
         p.MP = MP;
         p.NT = p.RB = 128 / MP;
@@ -761,10 +793,10 @@ static bool find_plan(Plan *best, const Shape &s, Mode mode, int sms) {
         for (int nqs = 1; nqs <= p.Q; ++nqs) {
             p.qc = cdiv(p.Q, nqs);
             p.qcp = up(p.qc, 16);
-            if (cdiv(p.Q, p.qc) != nqs || p.nacc * p.qcp > 256) continue;
+            if (cdiv(p.Q, p.qc) != nqs || 2 * p.qcp > 256) continue;
             if (nqs > 1 && p.qc < 8) break;
             p.nqs = nqs;
-            p.ybufs = 2 * p.nacc * p.qcp <= 256 ? 2 : 1;
+            p.ybufs = 4 * p.qcp <= 256 ? 2 : 1;
             p.c_chunk = up(p.qcp * K2b, 1024);
             const int64_t bytes_b = (int64_t)p.nblk * 128 * p.kb;
             const int64_t bytes_c = (int64_t)p.nac * p.nblk * p.c_chunk;
@@ -795,7 +827,7 @@ static bool find_plan(Plan *best, const Shape &s, Mode mode, int sms) {
             p.exact = p.M1 * 2 == p.kb && p.M2 % MP == 0 && p.ranks % p.RB == 0 &&
                       p.P == p.nac * p.AC && (p.AC * p.RB) % 64 == 0 && p.qc == p.qcp &&
                       p.Q % p.qc == 0;
-            p.tm_y = 512 - p.ybufs * p.nacc * p.qcp;
+            p.tm_y = 512 - p.ybufs * 2 * p.qcp;
             p.dbufs = gmin(kMaxD, p.tm_y / 128);
             p.g1 = gmin(kG1, gmin(p.dbufs, p.tbufs));
             p.off_c = (int)bytes_b;
