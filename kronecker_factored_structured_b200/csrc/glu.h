@@ -28,9 +28,9 @@ struct Plan {
     int nqs, qc, qcp, nks;    // c slices, columns per slice (and padded to 16), k slices
     int ybufs, stages, tbufs, dbufs;   // buffers of Y, x, T and D1
     int g1;                            // groups of epilogue-1 warps at work
-    int bias_smem, exact;              // biases in shared memory; no padding anywhere
+    int exact;                         // no padding anywhere
     int tm_y;                          // first TMEM column of Y
-    int off_c, off_t, off_x, off_bias, smem;   // shared memory: B^T at 0, C', T, x ring, biases
+    int off_c, off_t, off_x, smem;     // shared memory: B^T at 0, C', T, x ring
     int t_bytes, x_bytes, c_chunk;
     int ntiles, groups;       // row tiles, and CTAs per slice
 };

@@ -105,6 +105,14 @@ __device__ __forceinline__ void gate_pairs(int act, const float (&g)[8], const f
 #undef KRON_GATE
 }
 
+// Accumulator column (row of the packed C') that holds column c of a slice: in each group of 16 the
+// thread tq of a 16x256b load has the columns 2 tq, 2 tq + 1, 2 tq + 8 and 2 tq + 9, and these
+// hold c = tq, tq + 4, tq + 8 and tq + 12, so that one store of a warp covers four adjacent c.
+__device__ __forceinline__ int acc_column(int c) {
+    const int i = (c >> 2) & 3;
+    return (c & ~15) + 8 * (i >> 1) + 2 * (c & 3) + (i & 1);
+}
+
 // 16 lanes x 16 columns in the 16x256b pattern (tmem_load16x256_x4 with two repetitions) of two
 // accumulators, one wait for both.
 __device__ __forceinline__ void tmem_load16x256_x2(uint32_t ta, uint32_t tb, uint32_t (&r)[8],
@@ -130,8 +138,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const Plan &pl = g.pl;
-    const uint32_t sB = base, sC = base + pl.off_c, sT = base + pl.off_t, sX = base + pl.off_x,
-                   sBias = base + pl.off_bias;
+    const uint32_t sB = base, sC = base + pl.off_c, sT = base + pl.off_t, sX = base + pl.off_x;
     const uint32_t tail = base + pl.smem;
     uint8_t *tail_ptr = smem_raw + (tail - raw);
     auto bar = [&](int i) { return tail + 8u * i; };
@@ -258,7 +265,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             }
         }
         // stage-2 B operand of chunk ch = (ac, source, block), in the order of the tile's
-        // chunks: row c, K position il*AC + a % AC: C_i[a][c0 + c]
+        // chunks: row acc_column(c), K position il*AC + a % AC: C_i[a][c0 + c]
         {
             const int cmax = min(pl.qc, pl.Q - c0);
             const int outer = TR ? cmax : pl.P, len = TR ? pl.P : cmax, inner = (len + 7) >> 3;
@@ -300,13 +307,13 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                                     (kb >> 7) * (uint32_t)pl.qcp * 128u;
                 const uint32_t in = kb & 127u;
                 if constexpr (TR) {      // zeros behind p: inside the chunk's padding
-                    st_shared_v4(at + row * 128 + (in ^ ((row & 7) << 4)), wa[0], wa[1], wa[2],
-                                 wa[3]);
+                    const int c = acc_column(row);
+                    st_shared_v4(at + c * 128 + (in ^ ((c & 7) << 4)), wa[0], wa[1], wa[2], wa[3]);
                 } else {
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
                         if (t < left) {
-                            const int c = in8 + t;
+                            const int c = acc_column(in8 + t);
                             st_shared_u16(at + c * 128 + (in ^ ((c & 7) << 4)),
                                           (uint16_t)(wa[t >> 1] >> (16 * (t & 1))));
                         }
@@ -314,21 +321,6 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             }
         }
     }
-    // biases in fp32 by pairs of k: row c holds MP/2 times (gate k, k + 1; up k, k + 1), rows
-    // padded so that the 16-byte reads of epilogue 2 (k pairs x four rows c) meet different
-    // banks.  Where shared memory is short they are read from global memory at each use.
-    constexpr int kBiasRow = MP * 8 + 16;
-    const bool biased = MODE != kInput && g.bias != nullptr;
-    if (biased && pl.bias_smem)
-        for (int e = threadIdx.x; e < pl.qcp * MP * 2; e += kThreads) {
-            const int cl = e / (2 * MP), w = e % (2 * MP);
-            const int c = c0 + cl, k = k0 + (w >> 2) * 2 + (w & 1);
-            float v = 0.f;
-            if (cl < pl.qc && c < pl.Q && k < pl.M2)
-                v = __bfloat162float(
-                    g.bias[((w >> 1) & 1) * (size_t)g.out_ld + (size_t)c * pl.M2 + k]);
-            st_shared_u32(sBias + cl * kBiasRow + 4 * w, __float_as_uint(v));
-        }
     fence_proxy_async();
     tc_fence_before();
     __syncthreads();
@@ -561,7 +553,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
     } else {
         // ---------------- epilogue 2: Y (and bias, dH) -> outputs ----------------
         // A warp has 16 lanes of its quadrant and every second 16-column group; its items are
-        // (tile, group).  A thread holds, for the columns c = 2 tq, 2 tq + 1, + 8 and + 9 of the
+        // (tile, group).  A thread holds, for the columns c = tq, tq + 4, tq + 8 and tq + 12 of the
         // group, the pair of values k, k + 1.  For kPre the dH of an item are fetched two items
         // ahead.
         const int quad = warp & 3, wi = (warp - 4 - kE1) >> 2, w0c = wi >> 1;
@@ -570,10 +562,9 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
         const uint32_t y_addr = tmem + ((uint32_t)L16 << 16) + pl.tm_y;
         const bool k_ok = k < pl.M2;
         const int ni = ((pl.qcp >> 4) + 1 - w0c) >> 1;     // items per tile
-        const int qmax = min(pl.qc, pl.Q - c0) - 2 * tq;   // columns of this slice, from 2 tq on
+        const int qmax = min(pl.qc, pl.Q - c0) - tq;   // columns of this slice, from tq on
         const size_t lane_off =
-            (size_t)n_l * g.out_ld + (size_t)(c0 + 2 * tq + 16 * w0c) * pl.M2 + k;
-        const uint32_t bias_addr = sBias + (2 * tq + 16 * w0c) * kBiasRow + 8 * kl;
+            (size_t)n_l * g.out_ld + (size_t)(c0 + tq + 16 * w0c) * pl.M2 + k;
         const size_t tile_step = (size_t)NT * g.out_ld * pl.groups;   // to this CTA's next tile
         const size_t item_step = (size_t)32 * pl.M2;
         const int nlast = (int)g.N - n_l;                   // rows t NT below it exist
@@ -588,7 +579,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             const int left = row_ok ? qmax - (w0c + 2 * fi) * 16 : 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int c = (i & 1) + 8 * (i >> 1);
+                const int c = 4 * i;
                 to[i] = c < left ? __ldg(reinterpret_cast<const unsigned int *>(src + c * pl.M2))
                                  : 0u;
             }
@@ -597,9 +588,29 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
         __nv_bfloat16 *p0 = g.out0 + (size_t)group * NT * g.out_ld + lane_off;
         __nv_bfloat16 *p1 =
             MODE == kPre ? g.out1 + (size_t)group * NT * g.out_ld + lane_off : nullptr;
+        // biases of an item's four pairs: kept in registers where a warp has one item per tile,
+        // read again for each otherwise (from shared memory they took a seventh of its cycles)
+        uint32_t bias_g[4] = {}, bias_u[4] = {};
+        auto load_bias = [&](int item) {
+            const __nv_bfloat16 *p =
+                g.bias + (size_t)(c0 + tq + 16 * w0c + 32 * item) * pl.M2 + k;
+            const int left = k_ok ? qmax - (w0c + 2 * item) * 16 : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = 4 * i;
+                if (c < left) {
+                    bias_g[i] = __ldg(reinterpret_cast<const unsigned int *>(p + c * pl.M2));
+                    bias_u[i] =
+                        __ldg(reinterpret_cast<const unsigned int *>(p + g.out_ld + c * pl.M2));
+                }
+            }
+        };
+        const bool biased = MODE != kInput && g.bias != nullptr;
+        if (biased && ni > 0) load_bias(0);
         int t = group, item = 0, y = 0, yph = 0;
         // one item; false when the pipeline gave up
         auto process = [&](uint32_t (&d)[4]) -> bool {
+            if (biased && ni > 1) load_bias(item);
             if (item == 0) {
                 if (!warp_wait(bar(kYFull + y), yph, ab)) return false;
                 tc_fence_after();
@@ -607,8 +618,8 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             const int cb = (w0c + 2 * item) * 16;
             const uint32_t ya = y_addr + 2 * y * pl.qcp + cb;
             uint32_t w0[4], w1[4];
-            // registers 4 rep + (0, 1) hold k at the columns 8 rep + 2 tq (+ 1), 4 rep + (2, 3)
-            // hold k + 1
+            // registers 4 rep + (0, 1) hold k at the accumulator columns 8 rep + 2 tq (+ 1), that
+            // is at the i-th c for i = 2 rep (+ 1), and 4 rep + (2, 3) hold k + 1
             if constexpr (MODE == kInput) {
                 uint32_t r[8], q[8];
                 tmem_load16x256_x2(ya, ya + pl.qcp, r, q);
@@ -629,27 +640,10 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                     a[2 * i + 1] = __uint_as_float(r[o + 2]);
                     b[2 * i] = __uint_as_float(q[o]);
                     b[2 * i + 1] = __uint_as_float(q[o + 2]);
-                    if (biased) {
-                        const int c = (i & 1) + 8 * (i >> 1);
-                        uint32_t v[4] = {0, 0, 0, 0};
-                        if (pl.bias_smem) {
-                            ld_shared_v4(bias_addr + (32 * item + c) * kBiasRow, v);
-                        } else if (k_ok && cb + c < qmax) {
-                            const __nv_bfloat16 *p =
-                                g.bias + (size_t)(c0 + 2 * tq + cb + c) * pl.M2 + k;
-                            const uint32_t wg = __ldg(reinterpret_cast<const unsigned int *>(p));
-                            const uint32_t wu =
-                                __ldg(reinterpret_cast<const unsigned int *>(p + g.out_ld));
-                            v[0] = wg << 16;
-                            v[1] = wg & 0xFFFF0000u;
-                            v[2] = wu << 16;
-                            v[3] = wu & 0xFFFF0000u;
-                        }
-                        a[2 * i] += __uint_as_float(v[0]);
-                        a[2 * i + 1] += __uint_as_float(v[1]);
-                        b[2 * i] += __uint_as_float(v[2]);
-                        b[2 * i + 1] += __uint_as_float(v[3]);
-                    }
+                    a[2 * i] += __uint_as_float(bias_g[i] << 16);
+                    a[2 * i + 1] += __uint_as_float(bias_g[i] & 0xFFFF0000u);
+                    b[2 * i] += __uint_as_float(bias_u[i] << 16);
+                    b[2 * i + 1] += __uint_as_float(bias_u[i] & 0xFFFF0000u);
                 }
                 gate_pairs<MODE == kPre>(act, a, b, d, w0, w1);
             }
@@ -660,10 +654,10 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             if (t * NT < nlast && k_ok) {
                 const size_t o = (size_t)item * item_step;
                 const int left = qmax - cb;
-                if (left >= 10) {
+                if (left >= 13) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int c = (i & 1) + 8 * (i >> 1);
+                        const int c = 4 * i;
                         *reinterpret_cast<uint32_t *>(p0 + o + c * pl.M2) = w0[i];
                         if constexpr (MODE == kPre)
                             *reinterpret_cast<uint32_t *>(p1 + o + c * pl.M2) = w1[i];
@@ -671,7 +665,7 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
                 } else {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int c = (i & 1) + 8 * (i >> 1);
+                        const int c = 4 * i;
                         if (c < left) {
                             *reinterpret_cast<uint32_t *>(p0 + o + c * pl.M2) = w0[i];
                             if constexpr (MODE == kPre)
@@ -800,13 +794,8 @@ static bool find_plan(Plan *best, const Shape &s, Mode mode, int sms) {
             p.c_chunk = up(p.qcp * K2b, 1024);
             const int64_t bytes_b = (int64_t)p.nblk * 128 * p.kb;
             const int64_t bytes_c = (int64_t)p.nac * p.nblk * p.c_chunk;
-            int64_t bytes_bias = tr ? 0 : (int64_t)p.qcp * (MP * 8 + 16);
             int64_t left =
                 kSmemMax - (bytes_b + bytes_c + 2 * p.t_bytes + 2 * (int64_t)p.x_bytes);
-            // the biases only where that does not cost the third T buffer
-            p.bias_smem = !tr && left >= bytes_bias + p.t_bytes ? 1 : 0;
-            if (!p.bias_smem) bytes_bias = 0;
-            left -= bytes_bias;
             if (left < 0) continue;
             p.tbufs = p.stages = 2;
             // what is left over: a third T buffer, two more x stages, a fourth T buffer, x stages
@@ -833,8 +822,7 @@ static bool find_plan(Plan *best, const Shape &s, Mode mode, int sms) {
             p.off_c = (int)bytes_b;
             p.off_t = (int)(bytes_b + bytes_c);
             p.off_x = p.off_t + p.tbufs * p.t_bytes;
-            p.off_bias = p.off_x + p.stages * p.x_bytes;
-            p.smem = p.off_bias + (int)bytes_bias;
+            p.smem = p.off_x + p.stages * p.x_bytes;
             const int slices = p.nqs * p.nks;
             p.groups = (int)(tiles < sms / slices ? tiles : sms / slices);
             if (p.groups < 1) p.groups = 1;
