@@ -18,6 +18,7 @@
 // CTAs and held in registers, one read: 301, the barriers of the shorter pieces not covered).
 #include "../../include/kron_linear.h"
 #include "internal.h"
+#include "packed.cuh"
 
 #include <cuda_bf16.h>
 #include <math.h>
@@ -57,44 +58,6 @@ enum Exps {
     kFourth,  // tau = 4
     kTwo      // any other tau
 };
-
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// Two fp32 values in one 64-bit register pair, for the packed FP32 instructions: one issue slot
-// for two additions, multiplications or multiply-adds, each rounded as the scalar one.
-typedef uint64_t f2;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 ex2_2(f2 v) {
-    float lo, hi;
-    unpack2(v, lo, hi);
-    return pack2(ex2(lo), ex2(hi));
-}
 
 template <typename T> struct Vec;
 template <> struct Vec<float> {

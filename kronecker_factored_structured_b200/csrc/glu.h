@@ -4,6 +4,7 @@
 
 #include "../../include/kron_linear.h"
 #include "internal.h"
+#include "packed.cuh"
 
 namespace kron {
 namespace glu {
@@ -103,43 +104,49 @@ __device__ __forceinline__ float act_f32(int act, float g, float *d) {
     return f;
 }
 
-// Activation and derivative from hardware exponentials and reciprocals (about 2^-21 of the
-// value: far below the bfloat16 rounding of what is stored).
-__device__ __forceinline__ float sigmoid_fast(float g) {
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));   // e = inf: 0
-    return r;
+// Activation, and with GRAD its derivative, of two values, from hardware exponentials and
+// reciprocals (about 2^-21 of the value: far below the bfloat16 rounding of what is stored).
+__device__ __forceinline__ f2 sigmoid2(f2 g) {
+    // an exponential that overflows gives 0
+    return rcp_2(add2(ex2_2(mul2(g, dup2(-1.4426950408889634f))), dup2(1.f)));
 }
 
-template <int ACT>
-__device__ __forceinline__ float act_fast(float g, float *d) {
+template <int ACT, bool GRAD>
+__device__ __forceinline__ f2 act2(f2 g, f2 &d) {
     if constexpr (ACT == KRON_ACT_SILU) {
-        const float s = sigmoid_fast(g), f = g * s;
-        if (d) *d = s + f * (1.f - s);
+        const f2 s = sigmoid2(g), f = mul2(g, s);
+        if (GRAD) d = fma2(f, fma2(s, dup2(-1.f), dup2(1.f)), s);
         return f;
     } else if constexpr (ACT == KRON_ACT_SIGMOID) {
-        const float s = sigmoid_fast(g);
-        if (d) *d = s * (1.f - s);
+        const f2 s = sigmoid2(g);
+        if (GRAD) d = mul2(s, fma2(s, dup2(-1.f), dup2(1.f)));
         return s;
     } else if constexpr (ACT == KRON_ACT_GELU) {
-        const float c = 0.5f + 0.5f * erff(g * 0.70710678f);
-        if (d) {
-            float e;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * g * -0.72134752f));
-            *d = c + (e == 0.f ? 0.f : g * e * 0.39894228f);
+        float lo, hi;
+        unpack2(g, lo, hi);
+        const f2 c = fma2(pack2(erff(lo * 0.70710678f), erff(hi * 0.70710678f)), dup2(0.5f),
+                          dup2(0.5f));
+        if (GRAD) {
+            // g exp(-g^2 / 2) / sqrt(2 pi); nothing where the exponential vanishes
+            const f2 e = ex2_2(mul2(mul2(g, g), dup2(-0.72134752f)));
+            float e0, e1;
+            unpack2(e, e0, e1);
+            const f2 gz = pack2(e0 == 0.f ? 0.f : lo, e1 == 0.f ? 0.f : hi);
+            d = fma2(mul2(gz, e), dup2(0.39894228f), c);
         }
-        return g * c;
+        return mul2(g, c);
     } else {
         // (1 + tanh(v)) / 2 = sigmoid(2 v) with v = sqrt(2/pi) (g + 0.044715 g^3)
-        const float g2 = g * g;
-        const float s = sigmoid_fast(1.5957691f * g * (1.f + 0.044715f * g2));
-        if (d) {
-            const float w = s * (1.f - s);
-            *d = s + (w == 0.f ? 0.f : g * w * 1.5957691f * (1.f + 0.134145f * g2));
+        const f2 g2 = mul2(g, g);
+        const f2 s = sigmoid2(mul2(mul2(g, dup2(1.5957691f)), fma2(g2, dup2(0.044715f), dup2(1.f))));
+        if (GRAD) {
+            const f2 w = mul2(s, fma2(s, dup2(-1.f), dup2(1.f)));
+            float w0, w1, a, b;
+            unpack2(w, w0, w1);
+            unpack2(mul2(mul2(g, dup2(1.5957691f)), fma2(g2, dup2(0.134145f), dup2(1.f))), a, b);
+            d = fma2(w, pack2(w0 == 0.f ? 0.f : a, w1 == 0.f ? 0.f : b), s);
         }
-        return g * s;
+        return mul2(g, s);
     }
 }
 

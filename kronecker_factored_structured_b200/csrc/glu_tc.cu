@@ -70,39 +70,48 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) {
     return ((uint64_t)hi << 32) | lo;
 }
 
-template <int ACT, bool PRE>
-__device__ __forceinline__ void gated(float g, float u, float dh, float &o0, float &o1) {
-    if constexpr (PRE) {
-        float d;
-        const float f = act_fast<ACT>(g, &d);
-        o0 = dh * u * d;
-        o1 = dh * f;
-    } else {
-        o0 = act_fast<ACT>(g, nullptr) * u;
-    }
+// The two bfloat16 of a word, or of two words the lower or upper ones side by side, in fp32.
+__device__ __forceinline__ f2 lower2(uint32_t a, uint32_t b) {
+    return pack2(__uint_as_float(a << 16), __uint_as_float(b << 16));
+}
+__device__ __forceinline__ f2 upper2(uint32_t a, uint32_t b) {
+    return pack2(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u));
 }
 
-// Four pairs (k, k + 1) of one epilogue-2 item: pre-activations to packed outputs.
-template <bool PRE>
-__device__ __forceinline__ void gate_pairs(int act, const float (&g)[8], const float (&u)[8],
-                                           const uint32_t (&dh)[4], uint32_t (&w0)[4],
-                                           uint32_t (&w1)[4]) {
-#define KRON_GATE(ACT)                                                                        \
-    _Pragma("unroll") for (int t = 0; t < 4; ++t) {                                           \
-        float a0, a1, b0, b1;                                                                 \
-        gated<ACT, PRE>(g[2 * t], u[2 * t], __uint_as_float(dh[t] << 16), a0, b0);            \
-        gated<ACT, PRE>(g[2 * t + 1], u[2 * t + 1], __uint_as_float(dh[t] & 0xFFFF0000u), a1, \
-                        b1);                                                                  \
-        w0[t] = pack_bf16x2(a0, a1);                                                          \
-        if constexpr (PRE) w1[t] = pack_bf16x2(b0, b1);                                       \
+// One epilogue-2 item: accumulators r (gate) and q (up) of four columns at k and k + 1, two columns
+// side by side in packed arithmetic: pair (rep, kk) holds the columns 2 rep and 2 rep + 1 at
+// k + kk.  w0 and w1 get the outputs of each column as a pair (k, k + 1).
+template <int ACT, bool PRE>
+__device__ __forceinline__ void gate_item(const uint32_t (&r)[8], const uint32_t (&q)[8],
+                                          const uint32_t (&bg)[4], const uint32_t (&bu)[4],
+                                          const uint32_t (&dh)[4], uint32_t (&w0)[4],
+                                          uint32_t (&w1)[4]) {
+#pragma unroll
+    for (int rep = 0; rep < 2; ++rep) {
+        float o[2][2], p[2][2];      // [kk][column]
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const int i = 4 * rep + 2 * kk, c = 2 * rep;
+            const f2 g = add2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                              kk ? upper2(bg[c], bg[c + 1]) : lower2(bg[c], bg[c + 1]));
+            const f2 u = add2(pack2(__uint_as_float(q[i]), __uint_as_float(q[i + 1])),
+                              kk ? upper2(bu[c], bu[c + 1]) : lower2(bu[c], bu[c + 1]));
+            f2 d;
+            const f2 f = act2<ACT, PRE>(g, d);
+            if constexpr (PRE) {
+                const f2 h = kk ? upper2(dh[c], dh[c + 1]) : lower2(dh[c], dh[c + 1]);
+                unpack2(mul2(mul2(h, u), d), o[kk][0], o[kk][1]);
+                unpack2(mul2(h, f), p[kk][0], p[kk][1]);
+            } else {
+                unpack2(mul2(f, u), o[kk][0], o[kk][1]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            w0[2 * rep + c] = pack_bf16x2(o[0][c], o[1][c]);
+            if constexpr (PRE) w1[2 * rep + c] = pack_bf16x2(p[0][c], p[1][c]);
+        }
     }
-    switch (act) {
-        case KRON_ACT_SILU: KRON_GATE(KRON_ACT_SILU); break;
-        case KRON_ACT_GELU: KRON_GATE(KRON_ACT_GELU); break;
-        case KRON_ACT_GELU_TANH: KRON_GATE(KRON_ACT_GELU_TANH); break;
-        default: KRON_GATE(KRON_ACT_SIGMOID); break;
-    }
-#undef KRON_GATE
 }
 
 // Accumulator column (row of the packed C') that holds column c of a slice: in each group of 16 the
@@ -632,20 +641,19 @@ glu_tc_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ 
             } else {
                 uint32_t r[8], q[8];
                 tmem_load16x256_x2(ya, ya + pl.qcp, r, q);
-                float a[8], b[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int o = 4 * (i >> 1) + (i & 1);
-                    a[2 * i] = __uint_as_float(r[o]);
-                    a[2 * i + 1] = __uint_as_float(r[o + 2]);
-                    b[2 * i] = __uint_as_float(q[o]);
-                    b[2 * i + 1] = __uint_as_float(q[o + 2]);
-                    a[2 * i] += __uint_as_float(bias_g[i] << 16);
-                    a[2 * i + 1] += __uint_as_float(bias_g[i] & 0xFFFF0000u);
-                    b[2 * i] += __uint_as_float(bias_u[i] << 16);
-                    b[2 * i + 1] += __uint_as_float(bias_u[i] & 0xFFFF0000u);
+                constexpr bool PRE = MODE == kPre;
+                switch (act) {
+                    case KRON_ACT_SILU:
+                        gate_item<KRON_ACT_SILU, PRE>(r, q, bias_g, bias_u, d, w0, w1);
+                        break;
+                    case KRON_ACT_GELU:
+                        gate_item<KRON_ACT_GELU, PRE>(r, q, bias_g, bias_u, d, w0, w1);
+                        break;
+                    case KRON_ACT_GELU_TANH:
+                        gate_item<KRON_ACT_GELU_TANH, PRE>(r, q, bias_g, bias_u, d, w0, w1);
+                        break;
+                    default: gate_item<KRON_ACT_SIGMOID, PRE>(r, q, bias_g, bias_u, d, w0, w1); break;
                 }
-                gate_pairs<MODE == kPre>(act, a, b, d, w0, w1);
             }
             if (item == ni - 1) {
                 tc_fence_before();
