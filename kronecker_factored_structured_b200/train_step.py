@@ -23,6 +23,12 @@ part of the library.
     python -m kronecker_factored_structured_b200.train_step [--path tf32|f32|bf16]
         [--batches 256,20000] [--block 32] [--rank 4] [--warmup 10] [--steps 100] [--graph]
 
+Two more models train on a dense teacher's top logits instead of labels alone, as a compressed
+network is recovered from its original: `kron_distill`, the page's network, and
+`kron_glu_distill`, whose hidden layers are a gated feed-forward block (`KronGatedFFN`; paths
+f32 and bf16). The teacher is the dense baseline, its top five logits of the batch computed
+before the steps.
+
 Each configuration prints one JSON line with:
 - `ms_per_step`: CUDA events around the timed steps, on the launching stream;
 - `wall_ms_per_step`: host clock after a synchronize, as the page measures;
@@ -60,6 +66,21 @@ class KronMLP(nn.Module):
     def penalty(self):
         pen = self.l1.S.float().abs().sum() + self.l2.S.float().abs().sum()
         return pen.detach() if self.fused_l1 is not None else pen
+
+
+class KronGLUMLP(nn.Module):
+    """A gated feed-forward block of Kronecker layers, d -> d -> d, and the dense head."""
+
+    def __init__(self, d=1024, classes=10, block=32, rank=4, path="bf16", device="cuda"):
+        super().__init__()
+        self.ffn = kfs.KronGatedFFN(d, d, block, rank=rank, dtype=path, device=device)
+        self.head = nn.Linear(d, classes, device=device, dtype=kfs.native.io_dtype(path))
+
+    def forward(self, x):
+        return self.head(self.ffn(x))
+
+    def penalty(self):
+        return None
 
 
 class DenseMLP(nn.Module):
@@ -100,9 +121,16 @@ def _side_stream():
     return _SIDE
 
 
+def top_logits(teacher, x, top):
+    """(values float32, indices) of the `top` largest logits of each row."""
+    with torch.no_grad():
+        return teacher(x).float().topk(top)
+
+
 def time_model(model, batch, d, classes, lam, warmup, steps, dtype, seed=0, graph=False,
-               capturable=None):
-    """Times `steps` training steps after `warmup` untimed ones.  With graph=True the whole
+               capturable=None, teacher=None, top=5, temperature=2.0, label_weight=0.25):
+    """With a `teacher`, the loss is kfs.distill_loss against its `top` logits of each row, with
+    `label_weight` of cross-entropy.  Times `steps` training steps after `warmup` untimed ones.  With graph=True the whole
     step (forward, loss, backward, Adam) is captured once in a CUDA graph and replayed, so
     the host issues one launch per step instead of one per kernel.  Adam keeps its step
     count on the device (capturable) when graphed, or when asked to."""
@@ -115,10 +143,16 @@ def time_model(model, batch, d, classes, lam, warmup, steps, dtype, seed=0, grap
     opt = torch.optim.Adam(model.parameters(), lr=1e-3,
                            capturable=graph if capturable is None else capturable)
     loss_fn = nn.CrossEntropyLoss()
+    if teacher is not None:
+        values, indices = top_logits(teacher, x, top)
 
     def step():
         opt.zero_grad(set_to_none=True)
-        loss = loss_fn(model(x).float(), labels)
+        if teacher is not None:
+            loss = kfs.distill_loss(model(x), values, indices, labels, temperature=temperature,
+                                    label_weight=label_weight)
+        else:
+            loss = loss_fn(model(x).float(), labels)
         pen = model.penalty()
         if pen is not None:
             loss = loss + lam * pen
@@ -172,7 +206,8 @@ def main(argv=None):
     ap.add_argument("--no-dense", action="store_true", help="skip the dense baselines")
     ap.add_argument("--models", default=None,
                     help="comma-separated models to time, in this order (default: kron, "
-                         "kron_fused_l1, dense, dense_group_lasso; a name may repeat)")
+                         "kron_fused_l1, dense, dense_group_lasso; a name may repeat); also "
+                         "kron_distill, kron_glu_distill")
     ap.add_argument("--graph", action="store_true",
                     help="capture each model's whole step in a CUDA graph and replay it")
     args = ap.parse_args(argv)
@@ -192,6 +227,9 @@ def main(argv=None):
                                                  fused_l1=args.lam),
                 "dense": lambda: DenseMLP(d, classes, args.block, False, dtype),
                 "dense_group_lasso": lambda: DenseMLP(d, classes, args.block, True, dtype),
+                "kron_distill": lambda: KronMLP(d, classes, args.block, args.rank, args.path),
+                "kron_glu_distill": lambda: KronGLUMLP(d, classes, args.block, args.rank,
+                                                       args.path),
             }
             names = (args.models.split(",") if args.models else
                      ["kron", "kron_fused_l1"] + ([] if args.no_dense else
@@ -199,17 +237,21 @@ def main(argv=None):
             unknown = sorted(set(names) - set(make))
             if unknown:
                 raise SystemExit(f"unknown model(s) {unknown}; choose from {sorted(make)}")
+            if "kron_glu_distill" in names and args.path == "tf32":
+                raise SystemExit("kron_glu_distill runs on --path f32 and bf16")
             for name in names:
                 torch.manual_seed(0)
+                teacher = (DenseMLP(d, classes, args.block, False, dtype)
+                           if name.endswith("distill") else None)
                 model = make[name]()
                 r = time_model(model, batch, d, classes, args.lam, args.warmup, args.steps, dtype,
-                               graph=args.graph)
+                               graph=args.graph, teacher=teacher)
                 line = {"benchmark": "mlp_train_step", "model": name, "batch": batch,
                         "path": args.path, "block": args.block, "rank": args.rank,
                         "cuda_graph": args.graph,
                         "warmup": args.warmup, "steps": args.steps, **r}
                 print(json.dumps(line), flush=True)
-                del model
+                del model, teacher
                 torch.cuda.empty_cache()
     finally:
         torch.backends.cuda.matmul.allow_tf32 = old_tf32

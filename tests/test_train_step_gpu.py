@@ -104,3 +104,44 @@ def test_train_step_cuda_graph_replay_matches_eager():
         out[graph] = {n: to_np(p) for n, p in model.named_parameters()}
     for n in out[False]:
         assert rel_err(out[True][n], out[False][n]) <= 1e-5, n
+
+
+@pytest.mark.parametrize("name", ["kron_distill", "kron_glu_distill"])
+@pytest.mark.parametrize("path", ["f32", "bf16"])
+def test_distilled_models_run_and_their_gradients_are_the_formulas(path, name):
+    """The command's distilled models step eagerly and as a captured graph, and autograd through
+    the library's kernels gives the gradients of the same network in 64 bits."""
+    from kronecker_factored_structured_b200 import train_step as ts
+    import kronecker_factored_structured_b200 as kfs
+    dt = kfs.native.io_dtype(path)
+    torch.manual_seed(3)
+    teacher = ts.DenseMLP(1024, 10, dtype=dt)
+    model = (ts.KronMLP if name == "kron_distill" else ts.KronGLUMLP)(1024, 10, 32, 4, path)
+    for graph in (False, True):
+        r = ts.time_model(model, 96, 1024, 10, 1e-4, 1, 2, dt, graph=graph, teacher=teacher)
+        assert np.isfinite(r["final_loss"])
+    if name == "kron_distill":
+        return              # its layers' gradients are tested above, the loss's on its own
+    x = torch.randn(64, 1024, device="cuda").to(dt)
+    labels = torch.randint(0, 10, (64,), device="cuda")
+    values, indices = ts.top_logits(teacher, x, 5)
+    for p in model.parameters():
+        p.grad = None
+    kfs.distill_loss(model(x), values, indices, labels, temperature=2.0,
+                     label_weight=0.25).backward()
+    named = {n: p.detach().double().requires_grad_(True) for n, p in model.named_parameters()}
+    dense = lambda S, A, B: sum(torch.kron(S * A[i], B[i]) for i in range(4))  # noqa: E731
+    g, u = (x.double() @ dense(*(named["ffn.glu." + k][j] for k in "SAB"))
+            + named["ffn.glu.bias"][j] for j in (0, 1))
+    z = (g * torch.sigmoid(g) * u) @ dense(*(named["ffn.down." + k] for k in "SAB"))
+    z = (z + named["ffn.down.bias"]) @ named["head.weight"].t() + named["head.bias"]
+    p = torch.softmax(values.double() / 2, 1)
+    loss = (0.75 * 4 * (p * (p.log() - torch.log_softmax(z / 2, 1).gather(1, indices))).sum(1)
+            + 0.25 * torch.nn.functional.cross_entropy(z, labels, reduction="none")).mean()
+    want = torch.autograd.grad(loss, list(named.values()))
+    # f32: four operators in a row at 1e-5.  bf16: some fifteen roundings of 2^-8 / sqrt(3)
+    # behind a value, in the 2-norm, sqrt(15) 2.3e-3 = 9e-3, and twice that for gradients
+    # that are small sums of large terms
+    for (n, q), w in zip(model.named_parameters(), want):
+        err = (q.grad.double() - w).norm() / w.norm()
+        assert float(err) <= (1e-4 if path == "f32" else 2e-2), (n, float(err))

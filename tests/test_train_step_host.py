@@ -57,3 +57,15 @@ def test_time_model_refuses_mismatched_penalty_weight():
     model = KronMLP(d=64, classes=10, block=8, rank=2, path="f32", device="cpu", fused_l1=0.25)
     with pytest.raises(ValueError):
         time_model(model, 4, 64, 10, 0.5, warmup=0, steps=1, dtype=torch.float32)
+
+
+def test_glu_mlp_and_its_refusals():
+    from kronecker_factored_structured_b200.train_step import KronGLUMLP, main
+    model = KronGLUMLP(d=64, classes=10, block=8, rank=2, path="f32", device="cpu")
+    assert model.ffn.glu.A.shape == (2, 2, 8, 8) and model.penalty() is None
+    with pytest.raises((ValueError, RuntimeError)):
+        model(torch.randn(4, 64))
+    with pytest.raises(ValueError):
+        KronGLUMLP(d=64, block=8, path="tf32", device="cpu")
+    with pytest.raises(SystemExit):
+        main(["--models", "kron_glu_distill", "--path", "tf32"])
