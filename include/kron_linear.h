@@ -270,6 +270,9 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
  * the forward call.  bias may be NULL (none); dX and dbias may be NULL (skipped).  On KRON_BF16
  * T = X B and the pre-activations' gradients are rounded to bfloat16 between the products.
  * With N == 0 the forward is a no-op and the factor gradients are zero.
+ * h is not x, dX is not x, and no gradient is the tensor that it belongs to (the inputs are read
+ * until the last kernel): KRON_ERR_INVALID_ARG for the same pointer, and no other overlap of
+ * inputs and outputs either.  dX may be dH.
  * `workspace`: kron_glu_workspace_size(..., backward) bytes (forward: 0; may be 0 bytes, and
  * workspace then NULL), 256-byte aligned, owned by the caller; two calls that may run at the
  * same time need one each.  0 also means arguments that the call refuses.  N <= 2^30.
@@ -323,7 +326,7 @@ KRON_API kron_status_t kron_glu_backward(const void *x, const void *S, const voi
  *   dloss   [N] float32, the gradient of `loss`, NULL = ones
  *   dlogits rows ld_out elements apart, of the logits' type; may be the logits themselves
  *           (the same pointer and stride), and does not overlap them otherwise
- *   1e-3 <= temperature <= 1e3, 0 <= label_weight <= 1
+ *   0.05 <= temperature <= 1e3, 0 <= label_weight <= 1
  * kron_distill_step gives `loss` and the `dlogits` of the sum of `loss` in one call, reading
  * the logits from memory once.  Sums are formed in float32 in a fixed order: results are bitwise
  * reproducible.  No workspace.  Tensors need the alignment of their elements; rows that are

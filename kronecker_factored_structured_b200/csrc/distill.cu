@@ -507,8 +507,8 @@ kron_status_t check(const void *logits, int64_t ld, const void *values, const vo
     if (ld < V) return bad(KRON_ERR_INVALID_ARG, "row stride %g below V = %g", (double)ld, (double)V);
     if (index_bytes != 4 && index_bytes != 8)
         return bad(KRON_ERR_INVALID_ARG, "indices have 4 or 8 bytes (got %g)", index_bytes);
-    if (!(tau >= 1e-3 && tau <= 1e3))
-        return bad(KRON_ERR_INVALID_ARG, "the temperature must be in [1e-3, 1e3] (got %g)", tau);
+    if (!(tau >= 0.05 && tau <= 1e3))
+        return bad(KRON_ERR_INVALID_ARG, "the temperature must be in [0.05, 1e3] (got %g)", tau);
     if (!(lam >= 0.0 && lam <= 1.0))
         return bad(KRON_ERR_INVALID_ARG, "the label weight must be in [0, 1] (got %g)", lam);
     if (lam > 0.0 && !labels && N > 0)

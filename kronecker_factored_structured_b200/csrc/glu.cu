@@ -202,6 +202,7 @@ kron_status_t kron_glu_forward(const void *x, const void *S, const void *A, cons
     if (!a16(x) || !a16(S) || !a16(A) || !a16(B) || !a16(bias) || !a16(h))
         return bad(KRON_ERR_ALIGNMENT, "all tensors must be 16-byte aligned");
     if (N == 0) return KRON_OK;
+    if (h == x) return bad(KRON_ERR_INVALID_ARG, "h must not be x: not an in-place operation");
     const Shape s{N, p, q, m1, m2, r};
     st = check_workspace(workspace, workspace_bytes, need_bytes(s, dtype, false));
     if (st != KRON_OK) return st;
@@ -250,6 +251,8 @@ kron_status_t kron_glu_backward(const void *x, const void *S, const void *A, con
     if (!a16(x) || !a16(S) || !a16(A) || !a16(B) || !a16(bias) || !a16(dH) || !a16(dX) ||
         !a16(dS) || !a16(dA) || !a16(dB) || !a16(dbias))
         return bad(KRON_ERR_ALIGNMENT, "all tensors must be 16-byte aligned");
+    if ((N > 0 && dX == x && dX) || dS == S || dA == A || dB == B || (dbias && dbias == bias))
+        return bad(KRON_ERR_INVALID_ARG, "a gradient must not be the tensor that it belongs to");
     const Shape s{N, p, q, m1, m2, r};
     cudaStream_t cs = (cudaStream_t)stream;
     const size_t E = dtype == KRON_BF16 ? 2 : 4, pq = (size_t)p * q, mm = (size_t)m1 * m2;

@@ -380,8 +380,11 @@ def _need(t, name, dtype, shape, dev):
     raise ValueError(f"{name} is on {t.device}, not on {dev}")
 
 
-def _on_device(dev):
-    """Context in which dev is the current device."""
+def _on_device(dev, stream):
+    """Context in which dev is the current device, and memory that is allocated belongs to the
+    stream that the call runs on (a workspace may be handed out again once it returns)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
     return _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
@@ -456,7 +459,7 @@ def glu_forward(x, S, A, B, bias=None, activation="silu", dtype="bf16", out=None
     dtype "f32" or "bf16"."""
     sizes, t, dev = _glu_args(x, S, A, B, bias, activation, dtype)
     shape = (sizes[0], sizes[2] * sizes[4])
-    with _on_device(dev):
+    with _on_device(dev, stream):
         if out is None:
             out = torch.empty(shape, dtype=t, device=dev)
         else:
@@ -476,7 +479,7 @@ def glu_backward(x, S, A, B, dH, bias=None, activation="silu", dtype="bf16", nee
     N, p, q, m1, m2, r = sizes
     _need(dH, "dH", t, (N, q * m2), dev)
     g = dict(grads or {})
-    with _on_device(dev):
+    with _on_device(dev, stream):
         for k, shp, need in (("dX", (N, p * m1), need_dx), ("dS", (2, p, q), True),
                              ("dA", (2, r, p, q), True), ("dB", (2, r, m1, m2), True),
                              ("dbias", (2, q * m2), need_dbias)):
@@ -549,7 +552,7 @@ def distill_forward(logits, values, indices, labels=None, weights=None, temperat
     """Loss of each row against the teacher's top logits: dict(loss [N], lse [N][2])."""
     N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
                                               label_weight)
-    with _on_device(dev):
+    with _on_device(dev, stream):
         loss = torch.empty(N, dtype=torch.float32, device=dev)
         lse = torch.empty(N, 2, dtype=torch.float32, device=dev)
         _check(load().kron_distill_forward(*head, loss.data_ptr(), lse.data_ptr(), N, V, K,
@@ -567,7 +570,7 @@ def distill_backward(logits, values, indices, lse, dloss=None, labels=None, weig
     _need(lse, "lse", torch.float32, (N, 2), dev)
     if dloss is not None:
         _need(dloss, "dloss", torch.float32, (N,), dev)
-    with _on_device(dev):
+    with _on_device(dev, stream):
         out, ld_out = _dlogits(logits, out)
         _check(load().kron_distill_backward(*head, lse.data_ptr(), _at(dloss), out.data_ptr(),
                                             ld_out, N, V, K, temperature, label_weight, dtype,
@@ -581,7 +584,7 @@ def distill_step(logits, values, indices, labels=None, weights=None, temperature
     dict(loss [N], dlogits).  ``out`` may be the logits themselves."""
     N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
                                               label_weight)
-    with _on_device(dev):
+    with _on_device(dev, stream):
         loss = torch.empty(N, dtype=torch.float32, device=dev)
         out, ld_out = _dlogits(logits, out)
         _check(load().kron_distill_step(*head, loss.data_ptr(), out.data_ptr(), ld_out, N, V, K,

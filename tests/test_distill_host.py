@@ -30,7 +30,7 @@ COMMON = [(dict(dtype=1), 2), (dict(dtype=9), 2), (dict(N=-1), 1), (dict(N=1 << 
           (dict(V=0), 1), (dict(V=(1 << 30) + 1, ld=1 << 31, ld_out=1 << 31), 1),
           (dict(K=0), 1), (dict(K=1025), 2), (dict(ld=99), 1), (dict(index_bytes=2), 1),
           (dict(tau=0.0), 1), (dict(tau=-1.0), 1), (dict(tau=float("nan")), 1),
-          (dict(tau=2e3), 1), (dict(lam=-0.1), 1), (dict(lam=1.5), 1),
+          (dict(tau=2e3), 1), (dict(tau=0.01), 1), (dict(lam=-0.1), 1), (dict(lam=1.5), 1),
           (dict(lam=float("nan")), 1), (dict(labels=None), 1), (dict(logits=None), 1),
           (dict(values=None), 1), (dict(indices=None), 1), (dict(logits=ODD), 3),
           (dict(logits=V_(0x10002)), 3), (dict(logits=ODD, dtype=2), 3), (dict(values=ODD), 3),

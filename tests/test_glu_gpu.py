@@ -277,3 +277,64 @@ def test_gated_block_distilled_on_its_teachers_top_logits():
     torch.cuda.synchronize()
     for a, w in zip(again[:8], got[:8]):
         assert torch.equal(a, w)
+
+
+def test_offsets_beyond_32_bits():
+    """2,097,161 rows of 1024: element offsets pass 2^31 in x, h, dH and dX.  Rows are
+    independent, so the last ones are checked."""
+    N, shape = (1 << 21) + 9, (32, 32, 32, 32, 1)
+    d = make(64, *shape, seed=21)
+    x = torch.zeros(N, 1024, dtype=torch.bfloat16, device=DEV)
+    dH = torch.zeros(N, 1024, dtype=torch.bfloat16, device=DEV)
+    x[-64:], dH[-64:] = d["x"], d["dH"]
+    fac = (x, d["S"], d["A"], d["B"])
+    h = native.glu_forward(*fac, d["bias"])
+    g = native.glu_backward(*fac, dH, d["bias"])
+    native.device_error()
+    out = {"h": h[-64:], "dX": g["dX"][-64:], "dA": g["dA"], "dB": g["dB"], "dS": g["dS"],
+           "dbias": g["dbias"]}       # the other rows' gradients are zero
+    compare(out, reference(d, "silu"), "bf16")
+    assert not g["dX"][:-64][:: 4097].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_streams_at_once(dtype):
+    """Calls on streams of their own, given to the binding, with workspaces of their own."""
+    ds = [make(700 + 13 * i, 16, 24, 16, 32, 2, dtype=dtype, seed=i) for i in range(3)]
+    want = [run(d, "silu", dtype) for d in ds]
+    streams = [torch.cuda.Stream() for _ in ds]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for d, s in zip(ds, streams):
+            fac = (d["x"], d["S"], d["A"], d["B"])
+            g = native.glu_backward(*fac, d["dH"], d["bias"], dtype=dtype, stream=s)
+            g["h"] = native.glu_forward(*fac, d["bias"], dtype=dtype, stream=s)
+            got.append(g)
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(g[k], w[k]) for k in w)
+
+
+def test_given_workspace_and_outputs():
+    d = make(300, 9, 11, 24, 40, 3)
+    fac = (d["x"], d["S"], d["A"], d["B"])
+    n = native.glu_workspace_size(300, 9, 11, 24, 40, 3, "bf16", True)
+    ws = torch.full((n + 512,), 0x7F, dtype=torch.uint8, device=DEV)      # NaN everywhere
+    guard = ws[n:].clone()
+    g = native.glu_backward(*fac, d["dH"], d["bias"], workspace=ws[:n])
+    assert torch.equal(ws[n:], guard)
+    for k, v in native.glu_backward(*fac, d["dH"], d["bias"]).items():
+        assert torch.equal(v, g[k]), k
+    with pytest.raises(native.KronError):
+        native.glu_backward(*fac, d["dH"], d["bias"], workspace=ws[: n - 256])
+    # dX over dH
+    sq = make(77, 8, 8, 16, 16, 2)
+    fac = (sq["x"], sq["S"], sq["A"], sq["B"])
+    want = native.glu_backward(*fac, sq["dH"], sq["bias"])
+    got = native.glu_backward(*fac, dh := sq["dH"].clone(), sq["bias"], grads={"dX": dh})
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    with pytest.raises(native.KronError):
+        native.glu_backward(*fac, sq["dH"], sq["bias"], grads={"dX": sq["x"]})
+    with pytest.raises(native.KronError):
+        native.glu_forward(*fac, sq["bias"], out=sq["x"])

@@ -9,10 +9,11 @@ import kronecker_factored_structured_b200 as kfs
 from kronecker_factored_structured_b200 import native
 
 V = ctypes.c_void_p
-OK, ODD = V(0x10000), V(0x10008)
+OK, ODD = V(0x10000), V(0x10008)           # never dereferenced
+GX, GS, GA, GB, Gb, OUT = (V(0x20000 + 0x1000 * i) for i in range(6))
 
 
-def call(backward, x=OK, S=OK, A=OK, B=OK, bias=OK, h=OK, dX=OK, dS=OK, dA=OK, dB=OK, dbias=OK,
+def call(backward, x=OK, S=OK, A=OK, B=OK, bias=OK, h=OUT, dX=GX, dS=GS, dA=GA, dB=GB, dbias=Gb,
          N=8, p=4, q=4, m1=16, m2=16, r=2, act=0, dtype=2, flags=0, ws=OK, ws_bytes=1 << 40):
     lib = native.load()
     tail = (N, p, q, m1, m2, r, act, dtype, flags, ws, ws_bytes, None)
@@ -41,10 +42,15 @@ def test_rejects(backward, kwargs, status):
 
 @pytest.mark.parametrize("kwargs,status", [
     (dict(dS=None), 1), (dict(dA=None), 1), (dict(dB=None), 1), (dict(dX=ODD), 3),
-    (dict(dbias=ODD), 3), (dict(ws=None), 4), (dict(ws_bytes=100), 4), (dict(ws=V(0x10010)), 3)])
+    (dict(dbias=ODD), 3), (dict(dX=OK), 1), (dict(dS=OK), 1), (dict(dA=OK), 1), (dict(dB=OK), 1),
+    (dict(dbias=OK), 1), (dict(ws=None), 4), (dict(ws_bytes=100), 4), (dict(ws=V(0x10010)), 3)])
 @pytest.mark.parametrize("dtype", [0, 2])
 def test_backward_rejects(dtype, kwargs, status):
     assert call(True, dtype=dtype, **kwargs) == status
+
+
+def test_forward_is_not_in_place():
+    assert call(False, h=OK) == 1
 
 
 def test_forward_f32_wants_its_workspace():
