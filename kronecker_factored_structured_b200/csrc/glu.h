@@ -68,10 +68,10 @@ cudaError_t tc_run(const Plan &pl, const TcArgs &a, Mode mode, cudaStream_t st);
 // Dense weight gradients of the two projections, x^T [dg | du], in split row ranges, then
 // the factors' gradients from them.
 struct WgradPlan {
+    int direct;               // few rows: without dW
     int splits, tm;           // row ranges; rows of dW per tile
     int64_t rows_per_split;
     size_t part_floats;       // one split: [2][din][dout] and the column sums [2][dout]
-    int dbs;                  // ranges of (a) that dB's partial sums are split into
     size_t ws_bytes;
 };
 WgradPlan wgrad_plan(const Shape &s, int sms);

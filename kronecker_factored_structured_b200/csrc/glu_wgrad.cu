@@ -39,6 +39,9 @@ struct DwArgs {
     int din, dout, mt, nt;       // tiles along din, and along dout of one projection
     int tm;                      // rows of dW per tile: 256, or 128 where the tiles are few
     int sums;                    // whether the column sums are wanted
+    const __nv_bfloat16 *S, *A;
+    float *ct;                   // C_i[f] as [proj][f = (a, c)][rp], for the contraction
+    int pq, r, rp;
     int *device_error;
 };
 
@@ -136,6 +139,17 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
         const int quad = warp & 3, t = (warp - 2) * 32 + lane;
         float *part = g.part + (size_t)split * g.part_floats;
         const int half = (warp - 2) >> 2;
+        if (half == 1) {      // meanwhile: the factors side by side for the contraction
+            for (int e = blockIdx.x * 128 + t - 128; e < 2 * g.pq; e += gridDim.x * 128) {
+                const int proj2 = e >= g.pq, f = e - proj2 * g.pq;
+                const float sv = __bfloat162float(g.S[e]);
+                for (int i = 0; i < g.rp; ++i)
+                    g.ct[(size_t)e * g.rp + i] =
+                        i < g.r
+                            ? sv * __bfloat162float(g.A[((size_t)proj2 * g.r + i) * g.pq + f])
+                            : 0.f;
+            }
+        }
         if (sums && half == 0) {
             // columns 2t and 2t + 1 of the d tile, rows in order
             float s0 = 0.f, s1 = 0.f;
@@ -196,7 +210,7 @@ glu_dw_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CU
 
 // ---- contraction with the factors ----
 // dW is read as float4 along k, twice (second time from L2): once with a block per few (a, c)
-// for dC, once with a thread per four (j, k) for dB.
+// for dC, once with a block per eight (j, k) for dB; a third kind of block adds dbias.
 constexpr int kCt = 256;      // threads
 constexpr int kW = 2;         // places of dW read at a time
 constexpr int kJs = 4;        // parts of j (dC)
@@ -206,11 +220,13 @@ struct CtArgs {
     size_t part_floats;
     int splits;
     const __nv_bfloat16 *S, *A, *B;
-    __nv_bfloat16 *dS, *dA;
-    float *dbp;                  // [dbs][2][r][m1][m2]
-    int p, q, m1, m2, r, dout, dbs;
+    __nv_bfloat16 *dS, *dA, *dB, *dbias;
+    const float *sums;           // column sums of d, first split: [2][dout]
+    const float *ct;             // the factors as the first kernel left them
+    int rp;
+    int p, q, m1, m2, r, dout;
     int tk, cpb;                 // threads along k (m2 / 4), columns c per block (dC)
-    int dc_blocks;               // blocks of the first role
+    int dc_blocks, db_blocks;    // blocks of the first two kinds
 };
 
 // dW at W places, the splits added in order: 2 W loads in flight.
@@ -322,97 +338,213 @@ __device__ void dc_role(const CtArgs &g) {
         g.dS[proj * pq + (size_t)a * g.q + c0 + threadIdx.x] = __float2bfloat16_rn(ds);
 }
 
-// dB partial sums: a thread per four (j, k), a block per (projection, range of (a, c), ranks)
-template <int kRc>
+// dB: a block per (projection, ranks, kDbE float4 of (j, k)); kCt / kDbE threads share a float4, each
+// with a range of the (a, c), and their sums are added in order.
+template <int kRc, int kDbE>
 __device__ void db_role(const CtArgs &g, int blk) {
-    __shared__ float cs[kRc][64];      // C_i of up to 64 (a, c)
-    const int n4 = g.m1 * g.tk, eb = cdiv(n4, kCt), ib = cdiv(g.r, kRc);
-    const int e = blk % eb * kCt + threadIdx.x;
+    constexpr int kDbR = kCt / kDbE;
+    __shared__ float red[kDbR][kDbE * kRc * 4 + 1];
+    const int n4 = g.m1 * g.tk, eb = cdiv(n4, kDbE), ib = cdiv(g.r, kRc);
+    const int el = threadIdx.x % kDbE, range = threadIdx.x / kDbE;
+    const int e0 = blk % eb * kDbE, e = e0 + el;
     blk /= eb;
-    const int i0 = (blk % ib) * kRc;
-    blk /= ib;
-    const int range = blk % g.dbs, proj = blk / g.dbs;
+    const int i0 = blk % ib * kRc, proj = blk / ib;
     const int ni = min(kRc, g.r - i0), pq = g.p * g.q;
-    const int f0 = (int)((int64_t)pq * range / g.dbs), f1 = (int)((int64_t)pq * (range + 1) / g.dbs);
-    const bool live = e < n4;
-    const int j = live ? e / g.tk : 0, k = live ? 4 * (e - j * g.tk) : 0;
+    const size_t mm = (size_t)g.m1 * g.m2;
+    const int f0 = (int)((int64_t)pq * range / kDbR), f1 = (int)((int64_t)pq * (range + 1) / kDbR);
     float acc[kRc][4] = {};
-    for (int f = f0; f < f1; f += 64) {
-        const int nf = min(64, f1 - f);
-        __syncthreads();
-        for (int u = threadIdx.x; u < kRc * 64; u += kCt) {
-            const int i = u >> 6, w = u & 63;
-            cs[i][w] = i < ni && w < nf
-                           ? __bfloat162float(g.S[(size_t)proj * pq + f + w]) *
-                                 __bfloat162float(g.A[((size_t)proj * g.r + i0 + i) * pq + f + w])
-                           : 0.f;
-        }
-        __syncthreads();
-        if (live) {
-            int a = f / g.q, c = f - a * g.q;
-            const size_t o0 = ((size_t)proj * g.p * g.m1 + j) * g.dout + k;
-            for (int w = 0; w < nf; w += kW) {
-                size_t o[kW];
-                float4 v[kW];
+    if (e < n4) {
+        const int j = e / g.tk, k = 4 * (e - j * g.tk);
+        int a = f0 / g.q, c = f0 - a * g.q;
+        const size_t o0 = ((size_t)proj * g.p * g.m1 + j) * g.dout + k;
+        const float *ct = g.ct + (size_t)proj * pq * g.rp + i0;
+        for (int f = f0; f < f1; f += kW) {
+            size_t o[kW];
+            float4 v[kW], x[kW][kRc / 4];
 #pragma unroll
-                for (int t = 0; t < kW; ++t) {
-                    o[t] = o0 + (size_t)a * g.m1 * g.dout + (size_t)c * g.m2;
-                    if (w + t + 1 < nf && ++c == g.q) c = 0, ++a;
+            for (int t = 0; t < kW; ++t) {
+                o[t] = o0 + (size_t)a * g.m1 * g.dout + (size_t)c * g.m2;
+                const int ft = min(f + t, f1 - 1);
+#pragma unroll
+                for (int u = 0; u < kRc / 4; ++u)
+                    x[t][u] = f + t < f1 ? __ldg(reinterpret_cast<const float4 *>(
+                                               ct + (size_t)ft * g.rp + 4 * u))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (f + t + 1 < f1 && ++c == g.q) c = 0, ++a;
+            }
+            dw4(g, o, v);
+#pragma unroll
+            for (int t = 0; t < kW; ++t)
+#pragma unroll
+                for (int i = 0; i < kRc; ++i) {
+                    const float4 &xi = x[t][i / 4];
+                    const float w = i % 4 == 0 ? xi.x : i % 4 == 1 ? xi.y : i % 4 == 2 ? xi.z : xi.w;
+                    acc[i][0] = fmaf(v[t].x, w, acc[i][0]);
+                    acc[i][1] = fmaf(v[t].y, w, acc[i][1]);
+                    acc[i][2] = fmaf(v[t].z, w, acc[i][2]);
+                    acc[i][3] = fmaf(v[t].w, w, acc[i][3]);
                 }
-                dw4(g, o, v);
+        }
+    }
 #pragma unroll
-                for (int t = 0; t < kW; ++t)
-                    if (w + t < nf)
+    for (int i = 0; i < kRc; ++i)
 #pragma unroll
-                        for (int i = 0; i < kRc; ++i) {
-                            const float x = cs[i][w + t];
-                            acc[i][0] = fmaf(v[t].x, x, acc[i][0]);
-                            acc[i][1] = fmaf(v[t].y, x, acc[i][1]);
-                            acc[i][2] = fmaf(v[t].z, x, acc[i][2]);
-                            acc[i][3] = fmaf(v[t].w, x, acc[i][3]);
-                        }
+        for (int t = 0; t < 4; ++t) red[range][(i * kDbE + el) * 4 + t] = acc[i][t];
+    __syncthreads();
+    // a float4 of (j, k) is four neighbours of dB
+    for (int u = threadIdx.x; u < ni * kDbE * 4; u += kCt) {
+        const int i = u / (kDbE * 4), w = u % (kDbE * 4);
+        if (e0 * 4 + w >= n4 * 4) continue;
+        float v = 0.f;
+#pragma unroll 8
+        for (int s = 0; s < kDbR; ++s) v += red[s][u];
+        g.dB[((size_t)proj * g.r + i0 + i) * mm + (size_t)e0 * 4 + w] = __float2bfloat16_rn(v);
+    }
+}
+
+// dbias: the splits' column sums added in order.
+__device__ void bias_role(const CtArgs &g, int blk) {
+    const size_t e = (size_t)blk * kCt + threadIdx.x;
+    if (e >= (size_t)2 * g.dout) return;
+    float v = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s) v += g.sums[(size_t)s * g.part_floats + e];
+    g.dbias[e] = __float2bfloat16_rn(v);
+}
+
+template <int kRc, int kDbE>
+__global__ void __launch_bounds__(kCt, kRc == 4 ? 4 : 3) glu_contract_kernel(const CtArgs g) {
+    const int blk = blockIdx.x;
+    if (blk < g.dc_blocks) dc_role<kRc>(g);
+    else if (blk < g.dc_blocks + g.db_blocks) db_role<kRc, kDbE>(g, blk - g.dc_blocks);
+    else bias_role(g, blk - g.dc_blocks - g.db_blocks);
+}
+
+// ---- few rows: the vec trick's own order, without dW ----
+// dC_i[a,c] = sum_(n,k) T_i[n,a,k] d[n,c,k] with T = X B, dB_i[j,k] = sum_(n,a) X[n,a,j] U_i[n,a,k]
+// with U = C d, in fp32 on the CUDA cores, and nothing of dW's size is written or read.  Whole
+// backward calls, through dW and this way: 1 row of 4096 x 4096, r = 8: 324 and 61 us; 8 rows 328
+// and 135; 1 row of 2784 x 3192, r = 2: 123 and 53; 8 rows of 1024 x 1024, r = 4: 57 and 52; 8
+// rows of 1024 x 1280, r = 8: 65 and 59.  At 32 rows dW was faster for all of them.
+constexpr int kSmallRows = 8;
+
+struct SmArgs {
+    const __nv_bfloat16 *x, *d[2], *S, *A, *B;
+    __nv_bfloat16 *dS, *dA, *dB, *dbias;
+    int N, p, q, m1, m2, r;
+    int dc_blocks, db_blocks;
+};
+
+size_t small_smem(int N, int p, int m1, int m2, int r) {
+    const size_t dc = (size_t)N * ((size_t)r * m2 + m1), db = (size_t)N * p * 8;
+    return 4 * (dc > db ? dc : db);
+}
+
+// A block per (projection, a): T of this a for every term in shared memory, then a warp per c.
+__device__ void small_dc(const SmArgs &g, float *smem) {
+    const int a = blockIdx.x % g.p, proj = blockIdx.x / g.p, Nk = g.N * g.m2;
+    const int din = g.p * g.m1, dout = g.q * g.m2, pq = g.p * g.q, mm = g.m1 * g.m2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *T = smem, *X = smem + g.r * Nk;
+    for (int e = threadIdx.x; e < g.N * g.m1; e += kCt) {
+        const int n = e / g.m1, j = e - n * g.m1;
+        X[e] = __bfloat162float(g.x[(size_t)n * din + a * g.m1 + j]);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < g.r * Nk; e += kCt) {
+        const int i = e / Nk, rest = e - i * Nk, n = rest / g.m2, k = rest - n * g.m2;
+        const __nv_bfloat16 *b = g.B + ((size_t)proj * g.r + i) * mm + k;
+        float v = 0.f;
+#pragma unroll 8
+        for (int j = 0; j < g.m1; ++j)
+            v = fmaf(X[n * g.m1 + j], __bfloat162float(b[(size_t)j * g.m2]), v);
+        T[e] = v;
+    }
+    __syncthreads();
+    for (int c = warp; c < g.q; c += kCt / 32) {
+        const __nv_bfloat16 *d = g.d[proj] + c * g.m2;
+        const size_t pos = (size_t)proj * pq + a * g.q + c;
+        const float sv = __bfloat162float(g.S[pos]);
+        float ds = 0.f;
+        for (int i0 = 0; i0 < g.r; i0 += 4) {
+            float acc[4] = {};
+            for (int e = 2 * lane; e < Nk; e += 64) {
+                const int n = e / g.m2, k = e - n * g.m2;
+                const uint32_t w =
+                    *reinterpret_cast<const uint32_t *>(d + (size_t)n * dout + k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i0 + i < g.r) {
+                        const float2 t = *reinterpret_cast<const float2 *>(T + (i0 + i) * Nk + e);
+                        acc[i] = fmaf(t.x, __uint_as_float(w << 16), acc[i]);
+                        acc[i] = fmaf(t.y, __uint_as_float(w & 0xFFFF0000u), acc[i]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i0 + i < g.r) {
+                    for (int o = 16; o; o >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+                    const size_t ai = ((size_t)proj * g.r + i0 + i) * pq + a * g.q + c;
+                    if (lane == 0) g.dA[ai] = __float2bfloat16_rn(acc[i] * sv);
+                    ds = fmaf(acc[i], __bfloat162float(g.A[ai]), ds);
+                }
+        }
+        if (lane == 0) g.dS[pos] = __float2bfloat16_rn(ds);
+    }
+}
+
+// A block per (projection, term, eight k): U of these k in shared memory, then a thread per (j, k).
+__device__ void small_db(const SmArgs &g, int blk, float *U) {
+    const int k8 = g.m2 / 8, k0 = blk % k8 * 8, f = blk / k8, proj = f / g.r;   // f: flat term
+    const int din = g.p * g.m1, dout = g.q * g.m2, pq = g.p * g.q;
+    const __nv_bfloat16 *S = g.S + (size_t)proj * pq, *A = g.A + (size_t)f * pq;
+    for (int e = threadIdx.x; e < g.N * g.p; e += kCt) {
+        const int n = e / g.p, a = e - n * g.p;
+        const __nv_bfloat16 *d = g.d[proj] + (size_t)n * dout + k0;
+        float acc[8] = {};
+#pragma unroll 4
+        for (int c = 0; c < g.q; ++c) {
+            const float w =
+                __bfloat162float(S[a * g.q + c]) * __bfloat162float(A[a * g.q + c]);
+            const uint4 v = *reinterpret_cast<const uint4 *>(d + (size_t)c * g.m2);
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                acc[2 * t] = fmaf(w, __uint_as_float(u[t] << 16), acc[2 * t]);
+                acc[2 * t + 1] = fmaf(w, __uint_as_float(u[t] & 0xFFFF0000u), acc[2 * t + 1]);
             }
         }
-    }
-    if (live)
 #pragma unroll
-        for (int i = 0; i < kRc; ++i)
-            if (i < ni)
-                *reinterpret_cast<float4 *>(
-                    g.dbp + (((size_t)range * 2 + proj) * g.r + i0 + i) * g.m1 * g.m2 +
-                    (size_t)j * g.m2 + k) =
-                    make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-}
-
-template <int kRc>
-__global__ void __launch_bounds__(kCt, 4) glu_contract_kernel(const CtArgs g) {
-    if ((int)blockIdx.x < g.dc_blocks) dc_role<kRc>(g);
-    else db_role<kRc>(g, blockIdx.x - g.dc_blocks);
-}
-
-// dB and dbias: the ranges and splits, eight threads per value, each adding every eighth in
-// order, then their sums in order.
-__global__ void __launch_bounds__(kCt)
-glu_finish_kernel(const float *dbp, int dbs, size_t nb, __nv_bfloat16 *dB, const float *sums,
-                  size_t part_floats, int splits, size_t nbias, __nv_bfloat16 *dbias) {
-    __shared__ float red[8][32];
-    const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-    const size_t e = (size_t)blockIdx.x * 32 + lane;
-    float v = 0.f;
-    if (e < nb) {
-#pragma unroll 4
-        for (int s = part; s < dbs; s += 8) v += dbp[(size_t)s * nb + e];
-    } else if (e - nb < nbias) {
-        for (int s = part; s < splits; s += 8) v += sums[(size_t)s * part_floats + e - nb];
+        for (int t = 0; t < 8; ++t) U[e * 8 + t] = acc[t];
     }
-    red[part][lane] = v;
     __syncthreads();
-    if (part == 0 && e < nb + nbias) {
-        v = 0.f;
-#pragma unroll
-        for (int t = 0; t < 8; ++t) v += red[t][lane];
-        if (e < nb) dB[e] = __float2bfloat16_rn(v);
-        else dbias[e - nb] = __float2bfloat16_rn(v);
+    for (int e = threadIdx.x; e < g.m1 * 8; e += kCt) {
+        const int j = e >> 3, t = e & 7;
+        float v = 0.f;
+        for (int n = 0; n < g.N; ++n) {
+            const __nv_bfloat16 *x = g.x + (size_t)n * din + j;
+#pragma unroll 8
+            for (int a = 0; a < g.p; ++a)
+                v = fmaf(__bfloat162float(x[a * g.m1]), U[(n * g.p + a) * 8 + t], v);
+        }
+        g.dB[((size_t)f * g.m1 + j) * g.m2 + k0 + t] = __float2bfloat16_rn(v);
+    }
+}
+
+__global__ void __launch_bounds__(kCt) glu_small_grad_kernel(const SmArgs g) {
+    extern __shared__ __align__(16) float small_mem[];
+    const int blk = blockIdx.x;
+    if (blk < g.dc_blocks) {
+        small_dc(g, small_mem);
+    } else if (blk < g.dc_blocks + g.db_blocks) {
+        small_db(g, blk - g.dc_blocks, small_mem);
+    } else {
+        const int dout = g.q * g.m2, e = (blk - g.dc_blocks - g.db_blocks) * kCt + threadIdx.x;
+        if (e >= 2 * dout) return;
+        const __nv_bfloat16 *d = e < dout ? g.d[0] + e : g.d[1] + e - dout;
+        float v = 0.f;
+        for (int n = 0; n < g.N; ++n) v += __bfloat162float(d[(size_t)n * dout]);
+        g.dbias[e] = __float2bfloat16_rn(v);
     }
 }
 
@@ -424,6 +556,11 @@ static int ranks_at_a_time(int r) { return r <= 4 ? 4 : 8; }
 
 WgradPlan wgrad_plan(const Shape &s, int sms) {
     WgradPlan pl{};
+    // few rows take the direct kernel, as long as its tiles fit two blocks of shared memory per SM
+    if (s.N <= kSmallRows && small_smem((int)s.N, s.p, s.m1, s.m2, s.r) <= 100 * 1024) {
+        pl.direct = 1;
+        return pl;
+    }
     const int din = (int)s.d_in(), dout = (int)s.d_out();
     const int64_t tiles = (int64_t)cdiv(din, kTM) * 2 * cdiv(dout, kTN);
     int64_t splits = sms / tiles;
@@ -437,14 +574,8 @@ WgradPlan wgrad_plan(const Shape &s, int sms) {
     if (pl.splits < 1) pl.splits = 1;
     pl.tm = 2 * tiles * pl.splits <= sms ? 128 : kTM;
     pl.part_floats = pad64((size_t)2 * din * dout + 2 * (size_t)dout);
-    // dB: ranges of (a, c) for about four blocks per SM, at most 128 (their sums are added again)
-    const int64_t per = (int64_t)cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, ranks_at_a_time(s.r)) * 2;
-    int64_t dbs = (4 * sms + per - 1) / per;
-    if (dbs > 128) dbs = 128;
-    if (dbs > (int64_t)s.p * s.q) dbs = (int64_t)s.p * s.q;
-    pl.dbs = (int)dbs;
     pl.ws_bytes = 4 * (pl.part_floats * pl.splits +
-                       pad64((size_t)pl.dbs * 2 * s.r * s.m1 * s.m2));
+                       pad64((size_t)2 * s.p * s.q * up(s.r, ranks_at_a_time(s.r))));
     return pl;
 }
 
@@ -452,9 +583,40 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
                       const void *S, const void *A, const void *B, void *dS, void *dA, void *dB,
                       void *dbias, void *ws, const Shape &s, cudaStream_t st) {
     const int din = (int)s.d_in(), dout = (int)s.d_out();
+    cudaError_t e;
+    if (pl.direct) {
+        SmArgs m{};
+        m.x = static_cast<const __nv_bfloat16 *>(x);
+        m.d[0] = static_cast<const __nv_bfloat16 *>(dg);
+        m.d[1] = static_cast<const __nv_bfloat16 *>(du);
+        m.S = static_cast<const __nv_bfloat16 *>(S);
+        m.A = static_cast<const __nv_bfloat16 *>(A);
+        m.B = static_cast<const __nv_bfloat16 *>(B);
+        m.dS = static_cast<__nv_bfloat16 *>(dS);
+        m.dA = static_cast<__nv_bfloat16 *>(dA);
+        m.dB = static_cast<__nv_bfloat16 *>(dB);
+        m.dbias = static_cast<__nv_bfloat16 *>(dbias);
+        m.N = (int)s.N;
+        m.p = s.p;
+        m.q = s.q;
+        m.m1 = s.m1;
+        m.m2 = s.m2;
+        m.r = s.r;
+        m.dc_blocks = 2 * s.p;
+        m.db_blocks = 2 * s.r * (s.m2 / 8);
+        const size_t smem = small_smem(m.N, s.p, s.m1, s.m2, s.r);
+        launch_step() = "shared memory size";
+        e = cudaFuncSetAttribute(glu_small_grad_kernel,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        launch_step() = "factor-gradient launch";
+        const int blocks = m.dc_blocks + m.db_blocks + (dbias ? cdiv(2 * dout, kCt) : 0);
+        glu_small_grad_kernel<<<(unsigned)blocks, kCt, smem, st>>>(m);
+        return cudaGetLastError();
+    }
     CUtensorMap mx, mg, mu;
     launch_step() = "tensor map";
-    cudaError_t e = make_tmap_2d(&mx, x, true, s.N, din, 64, kTK, 128, false);
+    e = make_tmap_2d(&mx, x, true, s.N, din, 64, kTK, 128, false);
     if (e == cudaSuccess) e = make_tmap_2d(&mg, dg, true, s.N, dout, 64, kTK, 128, false);
     if (e == cudaSuccess) e = make_tmap_2d(&mu, du, true, s.N, dout, 64, kTK, 128, false);
     if (e != cudaSuccess) return e;
@@ -469,6 +631,12 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
     g.mt = cdiv(din, pl.tm);
     g.nt = cdiv(dout, kTN);
     g.sums = dbias != nullptr;
+    g.S = static_cast<const __nv_bfloat16 *>(S);
+    g.A = static_cast<const __nv_bfloat16 *>(A);
+    g.ct = g.part + pl.part_floats * pl.splits;
+    g.pq = s.p * s.q;
+    g.r = s.r;
+    g.rp = up(s.r, ranks_at_a_time(s.r));
     launch_step() = "device error word";
     g.device_error = device_error_ptr();
     if (!g.device_error) return cudaErrorInvalidSymbol;
@@ -490,33 +658,32 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
     c.B = static_cast<const __nv_bfloat16 *>(B);
     c.dS = static_cast<__nv_bfloat16 *>(dS);
     c.dA = static_cast<__nv_bfloat16 *>(dA);
-    c.dbp = g.part + pl.part_floats * pl.splits;
+    c.dB = static_cast<__nv_bfloat16 *>(dB);
+    c.dbias = static_cast<__nv_bfloat16 *>(dbias);
+    c.sums = g.part + (size_t)2 * din * dout;
+    c.ct = g.ct;
+    c.rp = g.rp;
     c.p = s.p;
     c.q = s.q;
     c.m1 = s.m1;
     c.m2 = s.m2;
     c.r = s.r;
     c.dout = dout;
-    c.dbs = pl.dbs;
     c.tk = s.m2 / 4;
     c.cpb = kCt / (c.tk * kJs);
     if (c.cpb < 1) return cudaErrorInvalidValue;       // m2 <= 256: checked by the entry points
     if (c.cpb > s.q) c.cpb = s.q;
     c.dc_blocks = 2 * s.p * cdiv(s.q, c.cpb);
-    const int db_blocks = cdiv(s.m1 * s.m2 / 4, kCt) * cdiv(s.r, ranks_at_a_time(s.r)) * pl.dbs * 2;
+    // dB: eight float4 per block where that still makes blocks for every SM, else two (32-byte
+    // reads of dW, four times the blocks): 1024 x 1024, r = 4 takes 20 us with two and 34 with eight
+    const int rc = ranks_at_a_time(s.r), n4 = s.m1 * s.m2 / 4, per = 2 * cdiv(s.r, rc);
+    const bool wide = per * cdiv(n4, 8) >= kRowParts;
+    c.db_blocks = per * cdiv(n4, wide ? 8 : 2);
+    const int blocks = c.dc_blocks + c.db_blocks + (dbias ? cdiv(2 * dout, kCt) : 0);
     launch_step() = "factor-gradient launch";
-    if (ranks_at_a_time(s.r) == 4)
-        glu_contract_kernel<4><<<(unsigned)(c.dc_blocks + db_blocks), kCt, 0, st>>>(c);
-    else
-        glu_contract_kernel<8><<<(unsigned)(c.dc_blocks + db_blocks), kCt, 0, st>>>(c);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const size_t nb = (size_t)2 * s.r * s.m1 * s.m2, nbias = dbias ? (size_t)2 * dout : 0;
-    launch_step() = "final sums launch";
-    glu_finish_kernel<<<(unsigned)((nb + nbias + 31) / 32), kCt, 0, st>>>(
-        c.dbp, pl.dbs, nb, static_cast<__nv_bfloat16 *>(dB),
-        g.part + (size_t)2 * din * dout, pl.part_floats, pl.splits, nbias,
-        static_cast<__nv_bfloat16 *>(dbias));
+    auto *f = rc == 4 ? (wide ? glu_contract_kernel<4, 8> : glu_contract_kernel<4, 2>)
+                      : (wide ? glu_contract_kernel<8, 8> : glu_contract_kernel<8, 2>);
+    f<<<(unsigned)blocks, kCt, 0, st>>>(c);
     return cudaGetLastError();
 }
 

@@ -79,7 +79,7 @@ def test_bf16_shapes(shape):
 
 
 @pytest.mark.parametrize("name", ACTS)
-@pytest.mark.parametrize("N", [2, 3, 4, 5, 16, 129, 2111])
+@pytest.mark.parametrize("N", [2, 3, 4, 5, 8, 9, 16, 129, 2111])
 def test_bf16_rows(N, name):
     d = make(N, 12, 20, 32, 32, 2, seed=N)
     compare(run(d, name, "bf16"), reference(d, name), "bf16")
