@@ -6,7 +6,7 @@
 //   loss = w [ (1 - lam) tau^2 sum_j p_j (log p_j - log q_{i_j}) + lam (lse(x) - x_label) ]
 //   dx_v = w dl [ (1 - lam) tau (q_v - sum_{j: i_j = v} p_j) + lam (softmax(x)_v - [v = label]) ]
 //
-// One CTA of 256 threads per row, six per SM.  Pass 1 reads the row with a running maximum m per
+// One CTA of 256 threads per row, six per SM (more threads where there are few rows).  Pass 1 reads the row with a running maximum m per
 // thread and the sums of exp((x - m)/tau) and exp(x - m); pass 2 (gradient) reads it again, from
 // L2, and writes the dense part c_t q + c_1 softmax(x); the K + 1 columns that the teacher and
 // the label touch are then overwritten by the thread that owns the first entry of the column,
@@ -30,7 +30,6 @@ kron_status_t report_failure(kron_status_t st, const char *msg);
 namespace {
 
 constexpr int kMaxK = 1024;      // teacher entries per row
-constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -178,6 +177,7 @@ struct RowSmem {
 };
 
 // Sum over the CTA in a fixed order; every thread gets it.
+template <int kThreads>
 __device__ __forceinline__ float block_sum(float v, float *red) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
@@ -187,6 +187,7 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     for (int i = 0; i < kThreads / 32; ++i) t += red[i];
     return t;
 }
+template <int kThreads>
 __device__ __forceinline__ float block_max(float v, float *red) {
     for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     __syncthreads();
@@ -197,8 +198,153 @@ __device__ __forceinline__ float block_max(float v, float *red) {
     return t;
 }
 
+// The dense part of a row's gradient, soft q + hard softmax(x), of one or two logits.
+template <int E> struct Dense {
+    f2 a, b, ct, c1, b1;
+    // a: log2(e) / tau (or log2(e), where only the label's term is there)
+    __device__ __forceinline__ Dense(float soft, float hard, float lse_t, float lse_1, float scale) {
+        // exp(x - lse_1) from q: (q exp(lse_t - lse_1/tau))^tau, the factor in [1, V]; with its
+        // power in the coefficient
+        const float lift = E == kSquare ? ex2((lse_t - 0.5f * lse_1) * kLog2e)
+                                        : E == kFourth ? ex2((lse_t - 0.25f * lse_1) * kLog2e)
+                                                       : 1.f;
+        const float l2 = lift * lift;
+        a = dup2(scale);
+        b = dup2(-lse_t * kLog2e);
+        b1 = dup2(-lse_1 * kLog2e);
+        ct = dup2(E == kOne ? soft + hard : soft);
+        c1 = dup2(E == kSquare ? hard * l2 : E == kFourth ? hard * (l2 * l2) : hard);
+    }
+    __device__ __forceinline__ f2 two(f2 v) const {
+        const f2 e = ex2_2(fma2(v, a, b));
+        if constexpr (E == kOne) return mul2(ct, e);
+        if constexpr (E == kSquare) return mul2(e, fma2(c1, e, ct));
+        if constexpr (E == kFourth) return mul2(e, fma2(mul2(c1, e), mul2(e, e), ct));
+        return fma2(c1, ex2_2(fma2(v, dup2(kLog2e), b1)), mul2(ct, e));
+    }
+    __device__ __forceinline__ float one(float v) const {
+        float lo, hi;
+        unpack2(two(dup2(v)), lo, hi);
+        return lo;
+    }
+};
+
+// Short rows (a classifier's logits): a warp per row, the teacher's entries in its own part of
+// shared memory.  20000 x 10 with its gradient takes 20 us; with a CTA per row it took
+// 121 us, nearly all of it starting and ending CTAs.
+constexpr int kShortV = 1024, kShortK = 64, kShortWarps = 8;
+
 template <typename T, int E, bool STATS, bool GRAD>
-__global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const Args g) {
+__global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const Args g, int64_t N) {
+    __shared__ int s_col[kShortWarps][kShortK];
+    __shared__ float s_prob[kShortWarps][kShortK], s_x[kShortWarps][kShortK];
+    using Vc = Vec<T>;
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, V = g.V, K = g.K;
+    const int64_t row = (int64_t)blockIdx.x * kShortWarps + wp;
+    if (row >= N) return;
+    const T *x = static_cast<const T *>(g.logits) + row * g.ld;
+    T *out = GRAD ? static_cast<T *>(g.dlogits) + row * g.ld_out : nullptr;
+    const float w = g.weights ? g.weights[row] : 1.f;
+    const float coef = GRAD ? (g.dloss ? w * g.dloss[row] : w) : w;
+    if (coef == 0.f) {
+        if (STATS && lane == 0) {
+            g.loss[row] = 0.f;
+            if (g.lse) g.lse[2 * row] = g.lse[2 * row + 1] = 0.f;
+        }
+        if (GRAD)
+            for (int v = lane; v < V; v += 32) Vc::put(out + v, 0.f);
+        return;
+    }
+    const bool hard_only = g.lam == 1.f;
+    const float inv_tau = hard_only ? 1.f : 1.f / g.tau, a = kLog2e * inv_tau;
+    int *col = s_col[wp];
+    float *prob = s_prob[wp], *xs = s_x[wp];
+    float tm = -INFINITY;
+    for (int j = lane; j < K; j += 32) {
+        const int64_t i = g.idx64 ? static_cast<const int64_t *>(g.indices)[row * K + j]
+                                  : static_cast<const int *>(g.indices)[row * K + j];
+        const bool there = i >= 0 && i < V;
+        col[j] = there ? (int)i : -1;
+        prob[j] = there ? g.values[row * K + j] : -INFINITY;
+        xs[j] = there ? Vc::get(x + i) : 0.f;
+        tm = fmaxf(tm, prob[j]);
+    }
+    const int64_t lab64 = g.labels ? g.labels[row] : -1;
+    const int label = lab64 >= 0 && lab64 < V ? (int)lab64 : -1;
+    const float xlab = label >= 0 ? Vc::get(x + label) : 0.f;
+    for (int o = 16; o; o >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, o));
+    float ts = 0.f;
+    for (int j = lane; j < K; j += 32) {
+        const float e = prob[j] == -INFINITY ? 0.f : ex2((prob[j] - tm) * (kLog2e / g.tau));
+        prob[j] = e;
+        ts += e;
+    }
+    for (int o = 16; o; o >>= 1) ts += __shfl_xor_sync(0xffffffffu, ts, o);
+    const bool any = ts != 0.f;
+    const float its = any ? 1.f / ts : 0.f;
+    float lse_t, lse_1;
+    if constexpr (STATS) {
+        Stat st{-INFINITY, 0.f, 0.f};
+        for (int v = lane; v < V; v += 32) add_one<E>(st, Vc::get(x + v), a);
+        for (int o = 16; o; o >>= 1) {
+            const Stat t = shuffle_xor<E>(st, o);
+            merge<E>(st, t, a);
+        }
+        const float lsum = logf(st.s);
+        lse_t = st.m * inv_tau + lsum;
+        lse_1 = E == kOne ? lse_t : st.m + logf(st.s1);
+        const float llse = logf(ts);
+        float kl = 0.f;
+        if (!hard_only)
+            for (int j = lane; j < K; j += 32)
+                if (col[j] >= 0 && prob[j] != 0.f)
+                    kl += prob[j] * its * ((g.values[row * K + j] - tm) * inv_tau - llse -
+                                           ((xs[j] - st.m) * inv_tau - lsum));
+        for (int o = 16; o; o >>= 1) kl += __shfl_xor_sync(0xffffffffu, kl, o);
+        if (lane == 0) {
+            float l = (1.f - g.lam) * g.tau * g.tau * kl;
+            if (g.lam != 0.f && label >= 0) l += g.lam * (lse_1 - xlab);
+            g.loss[row] = w * l;
+            if (g.lse) {
+                g.lse[2 * row] = lse_t;
+                g.lse[2 * row + 1] = lse_1;
+            }
+        }
+    } else {
+        lse_t = hard_only ? g.lse_in[2 * row + 1] : g.lse_in[2 * row];
+        lse_1 = g.lse_in[2 * row + 1];
+    }
+    if constexpr (GRAD) {
+        const float soft = hard_only || !any ? 0.f : coef * (1.f - g.lam) * g.tau;
+        const float hard = g.lam != 0.f && label >= 0 ? coef * g.lam : 0.f;
+        const Dense<E> dense(soft, hard, lse_t, lse_1, a);
+        const float share = soft == 0.f ? 0.f : soft * its;
+        __syncwarp();           // the row's gathers and entries are complete
+        for (int v = lane; v < V; v += 32) Vc::put(out + v, dense.one(Vc::get(x + v)));
+        __syncwarp();
+        bool listed = false;
+        for (int j = lane; j < K; j += 32) {
+            const int c = col[j];
+            if (c < 0) continue;
+            listed = listed || c == label;
+            float p = 0.f;
+            bool first = true;  // a column listed more than once: its first entry writes it
+            for (int k = 0; k < K; ++k)
+                if (col[k] == c) {
+                    if (k < j) first = false;
+                    p += prob[k];
+                }
+            if (first)
+                Vc::put(out + c, dense.one(xs[j]) - (share == 0.f ? 0.f : share * p) -
+                                     (c == label ? hard : 0.f));
+        }
+        listed = __any_sync(0xffffffffu, listed);
+        if (lane == 0 && label >= 0 && !listed) Vc::put(out + label, dense.one(xlab) - hard);
+    }
+}
+
+template <typename T, int E, bool STATS, bool GRAD, int kThreads>
+__global__ void __launch_bounds__(kThreads, (STATS ? 1536 : 2048) / kThreads) distill_kernel(const Args g) {
     __shared__ RowSmem sm;
     using Vc = Vec<T>;
     constexpr int n = Vc::n;
@@ -252,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const 
     const int64_t lab64 = g.labels ? g.labels[row] : -1;
     const int label = lab64 >= 0 && lab64 < V ? (int)lab64 : -1;
     const float xlab = label >= 0 ? Vc::get(x + label) : 0.f;
-    tm = block_max(tm, sm.redm);
+
+    tm = block_max<kThreads>(tm, sm.redm);
     float ts = 0.f;
     bool twice = false, listed = false;   // a column listed twice; the label's column listed
     for (int j = tid; j < K; j += kThreads) {
@@ -276,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const 
                 }
         }
     }
-    ts = block_sum(ts, sm.red);
+    ts = block_sum<kThreads>(ts, sm.red);
     const bool any = ts != 0.f;   // NaN counts: it has to show
     const float its = any ? 1.f / ts : 0.f;
 
@@ -359,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const 
                     kl += e * its * (lp - lq);
                 }
             }
-        kl = block_sum(kl, sm.red);
+        kl = block_sum<kThreads>(kl, sm.red);
         if (tid == 0) {
             float l = (1.f - g.lam) * g.tau * g.tau * kl;
             if (g.lam != 0.f && label >= 0) l += g.lam * (lse_1 - xlab);
@@ -378,36 +525,14 @@ __global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const 
     // ---- the gradient: c_t q + c_1 softmax(x), less the teacher's and the label's share
     const float soft = hard_only || !any ? 0.f : coef * (1.f - g.lam) * g.tau;
     const float hard = g.lam != 0.f && label >= 0 ? coef * g.lam : 0.f;
-    const float c_t = E == kOne ? soft + hard : soft;
-    const float b_t = -lse_t * kLog2e, b_1 = -lse_1 * kLog2e;
-    // exp(x - lse_1) from q: (q exp(lse_t - lse_1/tau))^tau, the factor in [1, V]; with its power
-    // in the coefficient: hard lift^tau q^tau
-    const float lift = E == kSquare ? ex2((lse_t - 0.5f * lse_1) * kLog2e)
-                                    : E == kFourth ? ex2((lse_t - 0.25f * lse_1) * kLog2e) : 1.f;
-    const float lift2 = lift * lift;
-    const float c_1 = E == kSquare ? hard * lift2 : E == kFourth ? hard * (lift2 * lift2) : hard;
-    // q (c_t + c_1 q^(tau - 1)) and so on, for two elements
-    const f2 a2 = pack2(a, a), b2 = pack2(b_t, b_t), ct2 = pack2(c_t, c_t), c12 = pack2(c_1, c_1);
-    auto dense2 = [&](f2 v) {
-        const f2 e = ex2_2(fma2(v, a2, b2));
-        if constexpr (E == kOne) return mul2(ct2, e);
-        if constexpr (E == kSquare) return mul2(e, fma2(c12, e, ct2));
-        if constexpr (E == kFourth) return mul2(e, fma2(mul2(c12, e), mul2(e, e), ct2));
-        const f2 l2 = pack2(kLog2e, kLog2e), d2 = pack2(b_1, b_1);
-        return fma2(c12, ex2_2(fma2(v, l2, d2)), mul2(ct2, e));
-    };
-    auto dense = [&](float v) {
-        float lo, hi;
-        unpack2(dense2(pack2(v, v)), lo, hi);
-        return lo;
-    };
+    const Dense<E> dense(soft, hard, lse_t, lse_1, a);
     // every gather of the row is done before it may be overwritten
     const bool dup = __syncthreads_or(twice), has_label = __syncthreads_or(listed);
     auto grad_vec = [&](const uint4 &u, int v) {
         f2 f[n / 2];
         Vc::unpack(u, f);
 #pragma unroll
-        for (int i = 0; i < n / 2; ++i) f[i] = dense2(f[i]);
+        for (int i = 0; i < n / 2; ++i) f[i] = dense.two(f[i]);
         T *o = out + head + v * n;
         if (same) {
             __stcs(reinterpret_cast<uint4 *>(o), Vc::pack(f));
@@ -430,9 +555,9 @@ __global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const 
         for (int i = 0; i < 4; ++i) grad_vec(u[i], v + i * kThreads);
     }
     for (; v < nv; v += kThreads) grad_vec(__ldcs(xv + v), v);
-    if (tid < head) Vc::put(out + tid, dense(Vc::get(x + tid)));
+    if (tid < head) Vc::put(out + tid, dense.one(Vc::get(x + tid)));
     const int tail = head + nv * n + tid;
-    if (tail < V) Vc::put(out + tail, dense(Vc::get(x + tail)));
+    if (tail < V) Vc::put(out + tail, dense.one(Vc::get(x + tail)));
     __syncthreads();
     const float share = soft == 0.f ? 0.f : soft * its;
     for (int j = tid; j < K; j += kThreads) {
@@ -449,10 +574,10 @@ __global__ void __launch_bounds__(kThreads, STATS ? 6 : 8) distill_kernel(const 
                 }
         }
         if (first)
-            Vc::put(out + c, dense(sm.x[j]) - (share == 0.f ? 0.f : share * p) -
+            Vc::put(out + c, dense.one(sm.x[j]) - (share == 0.f ? 0.f : share * p) -
                                  (c == label ? hard : 0.f));
     }
-    if (tid == 0 && label >= 0 && !has_label) Vc::put(out + label, dense(xlab) - hard);
+    if (tid == 0 && label >= 0 && !has_label) Vc::put(out + label, dense.one(xlab) - hard);
 }
 
 kron_status_t bad(kron_status_t st, const char *fmt, double a = 0, double b = 0) {
@@ -461,15 +586,30 @@ kron_status_t bad(kron_status_t st, const char *fmt, double a = 0, double b = 0)
     return report_failure(st, msg);
 }
 
-template <typename T, bool STATS, bool GRAD>
-cudaError_t launch_exps(int exps, unsigned grid, const Args &g, cudaStream_t st) {
-    switch (exps) {
-        case kOne: distill_kernel<T, kOne, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
-        case kSquare: distill_kernel<T, kSquare, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
-        case kFourth: distill_kernel<T, kFourth, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
-        default: distill_kernel<T, kTwo, STATS, GRAD><<<grid, kThreads, 0, st>>>(g); break;
-    }
+// Threads per row: with more than four rows per SM 256, with fewer as many as let all rows run at
+// once (515 x 50257 fp32 with its gradient: 58 us with 256 threads, 52 with 384).
+template <typename T, int E, bool STATS, bool GRAD>
+cudaError_t launch(int64_t N, const Args &g, cudaStream_t st) {
+    if (g.V <= kShortV && g.K <= kShortK)
+        distill_short_kernel<T, E, STATS, GRAD>
+            <<<(unsigned)((N + kShortWarps - 1) / kShortWarps), 32 * kShortWarps, 0, st>>>(g, N);
+    else if (N > 4 * kRowParts)
+        distill_kernel<T, E, STATS, GRAD, 256><<<(unsigned)N, 256, 0, st>>>(g);
+    else if (N > 2 * kRowParts)
+        distill_kernel<T, E, STATS, GRAD, 384><<<(unsigned)N, 384, 0, st>>>(g);
+    else
+        distill_kernel<T, E, STATS, GRAD, 768><<<(unsigned)N, 768, 0, st>>>(g);
     return cudaGetLastError();
+}
+
+template <typename T, bool STATS, bool GRAD>
+cudaError_t launch_exps(int exps, int64_t N, const Args &g, cudaStream_t st) {
+    switch (exps) {
+        case kOne: return launch<T, kOne, STATS, GRAD>(N, g, st);
+        case kSquare: return launch<T, kSquare, STATS, GRAD>(N, g, st);
+        case kFourth: return launch<T, kFourth, STATS, GRAD>(N, g, st);
+        default: return launch<T, kTwo, STATS, GRAD>(N, g, st);
+    }
 }
 
 template <bool STATS, bool GRAD>
@@ -477,10 +617,8 @@ kron_status_t run(const Args &g, int64_t N, kron_dtype_t dtype, void *stream) {
     const bool one = g.tau == 1.f || g.lam == 0.f || g.lam == 1.f;
     const int exps = one ? kOne : g.tau == 2.f ? kSquare : g.tau == 4.f ? kFourth : kTwo;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e =
-        dtype == KRON_BF16
-            ? launch_exps<__nv_bfloat16, STATS, GRAD>(exps, (unsigned)N, g, st)
-            : launch_exps<float, STATS, GRAD>(exps, (unsigned)N, g, st);
+    const cudaError_t e = dtype == KRON_BF16 ? launch_exps<__nv_bfloat16, STATS, GRAD>(exps, N, g, st)
+                                             : launch_exps<float, STATS, GRAD>(exps, N, g, st);
     if (e != cudaSuccess) {
         char msg[200];
         snprintf(msg, sizeof(msg), "distillation launch: %s", cudaGetErrorString(e));

@@ -102,7 +102,8 @@ def check_grad(got, ref, size, dtype):
 
 KW = dict(temperature=1.0, label_weight=0.0)
 MODES = [(1.0, 0.0), (1.0, 0.4), (2.0, 0.3), (4.0, 0.25), (1.5, 0.5), (3.0, 0.0), (2.0, 1.0)]
-SHAPES = [(1, 1, 1), (7, 2, 2), (6, 7, 3), (9, 10, 5), (8, 257, 64), (6, 1000, 300),
+# a warp per row (up to 1024 columns and 64 entries) and a CTA per row, on both sides of the edge
+SHAPES = [(13, 1024, 64), (13, 1025, 64), (13, 1024, 65), (2001, 10, 5), (1, 1, 1), (7, 2, 2), (6, 7, 3), (9, 10, 5), (8, 257, 64), (6, 1000, 300),
           (7, 4096, 1), (3, 50257, 64)]
 
 
@@ -123,9 +124,10 @@ def test_shapes(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [1021, 3001])
 @pytest.mark.parametrize("pad,offset", [(0, 1), (3, 0), (7, 5), (8, 0)])
-def test_strided_and_misaligned_rows(pad, offset, dtype):
-    N, V, K = 9, 1021, 17
+def test_strided_and_misaligned_rows(pad, offset, V, dtype):
+    N, K = 9, 17
     d = make(N, V, K, dtype, seed=3, pad=pad, offset=offset, idx=torch.int32)
     ref, grad, size = reference(d, 2.0, 0.3)
     kw = dict(labels=d["labels"], weights=d["weights"], temperature=2.0, label_weight=0.3)
@@ -156,9 +158,10 @@ def test_in_place(step):
     assert torch.equal(own, want["dlogits"])
 
 
-def test_columns_listed_more_than_once():
+@pytest.mark.parametrize("V", [300, 3000])
+def test_columns_listed_more_than_once(V):
     for dtype in (torch.float32, torch.bfloat16):
-        d = make(10, 300, 33, dtype, seed=6, duplicates=True)
+        d = make(10, V, 33, dtype, seed=6, duplicates=True)
         d["labels"][6] = int(d["indices"][6, 0])     # the label is one of them
         for tau, lam in ((1.0, 0.0), (2.0, 0.5)):
             ref, grad, size = reference(d, tau, lam)
@@ -177,10 +180,11 @@ def test_most_entries():
     check_grad(s["dlogits"], grad, size, torch.bfloat16)
 
 
-def test_infinities_and_nan():
+@pytest.mark.parametrize("V", [999, 1999])
+def test_infinities_and_nan(V):
     """-inf logits have probability zero; a row of weight zero is zero whatever it holds; a NaN
     shows in its own row only."""
-    d = make(6, 999, 8, torch.float32, seed=8, holes=False)
+    d = make(6, V, 8, torch.float32, seed=8, holes=False)
     x = d["logits"]
     x[0, 500:] = float("-inf")
     d["indices"][0] = torch.arange(8, device=DEV)
@@ -188,7 +192,7 @@ def test_infinities_and_nan():
     x[1, 3] = float("nan")
     x[2] = float("nan")
     d["weights"][2] = 0.0
-    x[3, :998] = -3e38
+    x[3, :V - 1] = -3e38
     x[4] = float("-inf")
     d["weights"][4] = 0.0
     kw = dict(labels=d["labels"], weights=d["weights"], temperature=2.0, label_weight=0.0)
