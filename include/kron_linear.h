@@ -259,12 +259,13 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
  *   S, dS [2][p][q];  A, dA [2][r][p][q];  B, dB [2][r][m1][m2];  bias, dbias [2][q*m2]
  *   x, dX [N][p*m1];  h, dH [N][q*m2]
  * `activation` is a kron_activation_t.  flags must be 0.
- *   KRON_F32   every tensor float32, exact FP32 arithmetic (the layer's CUDA-core kernels)
+ *   KRON_F32   every tensor float32, exact FP32 arithmetic on the CUDA cores; m1 and m2
+ *              multiples of 4
  *   KRON_BF16  every tensor bfloat16, the gradients too (each rounded once from float32);
  *              tcgen05 tensor cores: both projections, the activation and the product in one
  *              kernel.  Sizes are run-time values; m1 and m2 multiples of 8 up to 256, p and q
- *              at most 1024, and the factors of some slice of the layer have to fit shared memory, else
- *              KRON_ERR_UNSUPPORTED (about r p <= 1000 and r m1 <= 2000)
+ *              at most 1024, and the factors of some slice of the layer have to fit shared
+ *              memory, else KRON_ERR_UNSUPPORTED (about r p <= 1000 and r m1 <= 2000)
  *   KRON_TF32  KRON_ERR_UNSUPPORTED
  * Backward: gradients of <dH, h>; the pre-activations are formed again, nothing is kept from
  * the forward call.  bias may be NULL (none); dX and dbias may be NULL (skipped).  On KRON_BF16
@@ -273,9 +274,10 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
  * h is not x, dX is not x, and no gradient is the tensor that it belongs to (the inputs are read
  * until the last kernel): KRON_ERR_INVALID_ARG for the same pointer, and no other overlap of
  * inputs and outputs either.  dX may be dH.
- * `workspace`: kron_glu_workspace_size(..., backward) bytes (forward: 0; may be 0 bytes, and
- * workspace then NULL), 256-byte aligned, owned by the caller; two calls that may run at the
- * same time need one each.  0 also means arguments that the call refuses.  N <= 2^30.
+ * `workspace`: kron_glu_workspace_size(..., backward) bytes, 256-byte aligned, owned by the
+ * caller; two calls that may run at the same time need one each.  The forward needs 0 bytes
+ * (workspace may then be NULL), but for some shapes and many rows in KRON_F32.  0 also means
+ * arguments that the call refuses.  N <= 2^30.
  * Results are bitwise reproducible on one GPU model.  Everything else as for the layer.
  */
 typedef enum {

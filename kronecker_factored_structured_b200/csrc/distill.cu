@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
 }
 
 template <typename T, int E, bool STATS, bool GRAD, int kThreads>
-__global__ void __launch_bounds__(kThreads, (STATS ? 1536 : 2048) / kThreads) distill_kernel(const Args g) {
+__global__ void __launch_bounds__(kThreads, (STATS ? 1536 : 2048) / kThreads)
+distill_kernel(const Args g) {
     __shared__ RowSmem sm;
     using Vc = Vec<T>;
     constexpr int n = Vc::n;
@@ -617,8 +618,9 @@ kron_status_t run(const Args &g, int64_t N, kron_dtype_t dtype, void *stream) {
     const bool one = g.tau == 1.f || g.lam == 0.f || g.lam == 1.f;
     const int exps = one ? kOne : g.tau == 2.f ? kSquare : g.tau == 4.f ? kFourth : kTwo;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == KRON_BF16 ? launch_exps<__nv_bfloat16, STATS, GRAD>(exps, N, g, st)
-                                             : launch_exps<float, STATS, GRAD>(exps, N, g, st);
+    const cudaError_t e = dtype == KRON_BF16
+                              ? launch_exps<__nv_bfloat16, STATS, GRAD>(exps, N, g, st)
+                              : launch_exps<float, STATS, GRAD>(exps, N, g, st);
     if (e != cudaSuccess) {
         char msg[200];
         snprintf(msg, sizeof(msg), "distillation launch: %s", cudaGetErrorString(e));

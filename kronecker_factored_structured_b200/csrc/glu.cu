@@ -6,7 +6,7 @@
 //
 // BF16: one tensor-core kernel forward; backward: the pre-activations' gradients, dX, the dense
 // weight gradients and their contraction (glu_tc.cu, glu_wgrad.cu).  F32: one CUDA-core kernel
-// for both projections and the activation (simt_f32.cu), or the layer's kernels for each with the
+// for both projections and the activation (glu_f32.cu), or the layer's kernels for each with the
 // elementwise kernels below; backward by the layer's kernels over both projections at once; FFMA
 // bound.
 #include "glu.h"
@@ -115,11 +115,13 @@ kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int ac
     const Shape s{N > 0 ? N : 1, p, q, m1, m2, r};
     Plan pl;
     if (dtype == KRON_BF16) {
-        if (p > 1024 || q > 1024 || m1 > 256 || m2 > 256 || !glu::tc_plan(&pl, s, glu::kForward, kRowParts) ||
+        if (p > 1024 || q > 1024 || m1 > 256 || m2 > 256 ||
+            !glu::tc_plan(&pl, s, glu::kForward, kRowParts) ||
             !glu::tc_plan(&pl, s, glu::kInput, kRowParts))
             return bad(KRON_ERR_UNSUPPORTED,
                        "no tensor-core kernel for p=%d q=%d m1=%d m2=%d r=%d: blocks above 256 or "
-                       "factors that do not fit shared memory (KRON_F32 runs any shape)", p, q, m1, m2, r);
+                       "factors that do not fit shared memory (KRON_F32 runs any shape)",
+                       p, q, m1, m2, r);
     } else if (simt_forward_rows(s) <= 0 || simt_backward_rows(s) <= 0) {
         return bad(KRON_ERR_UNSUPPORTED,
                    "no kernel for p=%d q=%d m1=%d m2=%d r=%d: the FP32 tile does not fit shared "
@@ -129,11 +131,12 @@ kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int ac
 }
 
 // F32: whether both projections run in one kernel with the activation.  The compiled shape's own
-// kernels are faster than that one where they have rows to fill the SMs with: 20000 rows, r = 4,
-// MEASURE_FUSED us in one kernel and MEASURE_TWO us in two and an elementwise pass.
+// kernels are faster than that one where they have rows to fill the SMs with: forward of 1024 rows
+// 57 us in one kernel and 73 in two and an elementwise pass, 2368 rows 139 and 105, 20000 rows 913
+// and 613; backward 211 and 226, 395 and 357, 2608 and 2278.
 bool fused_f32(const Shape &s) {
     const bool compiled = s.p == 32 && s.q == 32 && s.m1 == 32 && s.m2 == 32 && s.r == 4;
-    return glu::simt_pre_supported(s) && !(compiled && s.N >= 8 * 2 * kRowParts);
+    return glu::f32_pre_supported(s) && !(compiled && s.N >= 10 * kRowParts);
 }
 
 // Workspace: forward F32 [g] unless fused; backward F32 [g][u][dX of up][partials of both];
@@ -223,7 +226,7 @@ kron_status_t kron_glu_forward(const void *x, const void *S, const void *A, cons
         e = glu::tc_run(pl, a, glu::kForward, cs);
     } else {
         if (fused_f32(s)) {
-            e = glu::simt_pre(x, S, A, B, bias, nullptr, h, nullptr, s, activation, false, cs);
+            e = glu::f32_pre(x, S, A, B, bias, nullptr, h, nullptr, s, activation, false, cs);
         } else {
             e = pre_f32(x, S, A, B, bias, (float *)workspace, (float *)h, s, cs);
             if (e == cudaSuccess) {
@@ -306,7 +309,7 @@ kron_status_t kron_glu_backward(const void *x, const void *S, const void *A, con
     const int parts = (int)(kron_linear_workspace_size(N, p, q, m1, m2, r, KRON_F32) /
                             (partial_stride(s) * sizeof(float)));
     if (fused_f32(s)) {
-        e = glu::simt_pre(x, S, A, B, bias, dH, g, u, s, activation, true, cs);
+        e = glu::f32_pre(x, S, A, B, bias, dH, g, u, s, activation, true, cs);
     } else {
         e = pre_f32(x, S, A, B, bias, g, u, s, cs);
         if (e == cudaSuccess) {

@@ -36,13 +36,13 @@ struct Plan {
     int ntiles, groups;       // row tiles, and CTAs per slice
 };
 
-// ---- exact FP32 (simt_f32.cu) ----
+// ---- exact FP32 (glu_f32.cu, simt_f32.cu) ----
 // Whether both projections, the activation and the product of this shape run as one kernel.
-bool simt_pre_supported(const Shape &s);
+bool f32_pre_supported(const Shape &s);
 // h (grad = false), or dg and du from dH (grad = true); factors stacked gate, up.
-cudaError_t simt_pre(const void *x, const void *S, const void *A, const void *B, const void *bias,
-                     const void *dH, void *out0, void *out1, const Shape &s, int activation,
-                     bool grad, cudaStream_t st);
+cudaError_t f32_pre(const void *x, const void *S, const void *A, const void *B, const void *bias,
+                    const void *dH, void *out0, void *out1, const Shape &s, int activation,
+                    bool grad, cudaStream_t st);
 // simt_backward of both projections: gradients G0, G1 into dX0, dX1 (may be null) and the
 // partials of gate and up, parts x partial_stride floats each, into ws.
 cudaError_t simt_backward_pair(const void *x, const void *S, const void *A, const void *B,

@@ -14,14 +14,18 @@
 // (12 warps) moves a chunk TMEM -> bf16 -> shared memory, which is the permute of the vec trick;
 // epilogue 2 (16 warps) has g and u of one (n, k, c) side by side.  For kInput the kernel runs
 // with transposed factors, dg against the gate's and du against the up's ranks, and the two
-// accumulators are added.  T is rounded to BF16 between the stages, as in the layer's own kernels: half
-// a step, 2^-8 of each term.
+// accumulators are added.  T is rounded to BF16 between the stages, as in the layer's own
+// kernels: half a step, 2^-8 of each term.
 //
 // A CTA holds the factors of one (k slice, c slice) in shared memory for its life and streams
 // row tiles; slices exist where the factors do not fit at once, and for few rows, where the
 // set-up of the factors is what takes the time.  Stage 1 is repeated for each c slice.
-// Bound by shared memory: per chunk 32 KB of T stored and 32 KB read back, 512 of about 770
-// cycles at 128 B/clk for the 32 x 32 blocks, against 256 cycles of MMA.
+// Bound by the SM's shared-memory pipe and issue slots: per chunk 32 KB of T are stored and read
+// back beside the MMAs' other operands, 512 cycles at 128 B/clk for the 32 x 32 blocks against
+// 256 cycles of MMA.  20000 x 1024, r = 4: 44 us, 74% of the pipe's cycles (36 the warps', 38 the
+// tensor core's), 75% of the issue slots, 0.95 TB/s of HBM; 16384 x 4096, r = 8: 390 us, 705
+// TFLOP/s.  Backward of the 20000 rows: pre-activations' gradients 66 us (epilogue 2's latency:
+// three reads and two stores per element), dX 43.
 #include "glu.h"
 #include "tc_gen_common.cuh"
 
@@ -749,8 +753,8 @@ const void *kernel_of(Mode m) {
 static double mma_cycles(int n) { return n > 208 ? n * 0.5 : 70 + n * 0.13; }
 
 // Chooses MP, the c slices and the ring by an estimate of the kernel's time: per chunk the
-// larger of its shared-memory cycles (128 B each) and its MMA cycles and about 80 of hand-over, per tile at least epilogue 2's time, per CTA the packing of the
-// factors.  More slices mean less packing per CTA and room for the factors, and more repeats of
+// larger of its shared-memory cycles (128 B each) and its MMA cycles and about 80 of hand-over,
+// per tile at least epilogue 2's time, per CTA the packing of the factors.  More slices mean less packing per CTA and room for the factors, and more repeats of
 // stage 1 and of the reads of x.
 static bool find_plan(Plan *best, const Shape &s, Mode mode, int sms) {
     double best_cost = 0;
@@ -882,14 +886,16 @@ bool tc_plan(Plan *best, const Shape &s, Mode mode, int sms) {
 }
 
 cudaError_t tc_run(const Plan &pl, const TcArgs &a, Mode mode, cudaStream_t st) {
+    // the error word's look-up binds a context to this thread, which the encoder needs
+    launch_step() = "device error word";
+    int *const device_error = device_error_ptr();
+    if (!device_error) return cudaErrorInvalidSymbol;
     launch_step() = "tensor map";
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaSetDevice(dev);   // binds the context for the driver call
     CUtensorMap m0, m1;
-    if (e == cudaSuccess) e = map_rows(&m0, a.src0, a.N, pl);
-    if (e == cudaSuccess) e = map_rows(&m1, mode == kInput ? a.src1 : a.src0, a.N, pl);
+    cudaError_t e = map_rows(&m0, a.src0, a.N, pl);
+    if (e == cudaSuccess && mode == kInput) e = map_rows(&m1, a.src1, a.N, pl);
     if (e != cudaSuccess) return e;
+    if (mode != kInput) m1 = m0;
     KArgs k{};
     k.pl = pl;
     k.S = static_cast<const __nv_bfloat16 *>(a.S);
@@ -903,9 +909,7 @@ cudaError_t tc_run(const Plan &pl, const TcArgs &a, Mode mode, cudaStream_t st) 
     k.pq = pl.P * pl.Q;
     k.mm = pl.M1 * pl.M2;
     k.out_ld = pl.Q * pl.M2;
-    launch_step() = "device error word";
-    k.device_error = device_error_ptr();
-    if (!k.device_error) return cudaErrorInvalidSymbol;
+    k.device_error = device_error;
     const void *f = pl.MP == 16   ? kernel_of<16>(mode)
                     : pl.MP == 32 ? kernel_of<32>(mode)
                     : pl.MP == 64 ? kernel_of<64>(mode)

@@ -404,110 +404,6 @@ kron_fwd_simt_kernel(const TI *__restrict__ x, const TI *__restrict__ S,
     }
 }
 
-// Both projections of the gated half (glu.h), the activation and the product of R rows: the two
-// stages of the kernel above for G of the 2r terms at a time (gate's first, then up's), and then
-// h = act(g) u, or for GRAD dg = dH u act'(g) and du = dH act(g).  The rows of x are loaded once.
-// Bound by shared-memory reads (8 words per 16 multiply-adds) and, for some hundreds of rows, by
-// the latency of its phases: 1000 x 1024, r = 2 takes 45 us with 4-row tiles (250 CTAs, two per
-// SM); the two projections as separate launches of 8-row tiles and an elementwise pass took 55.
-struct GluLayout {
-    int R, G, ldx, ldb, ldc, ldt;
-    size_t offX, offB, offC, offT, offG, offU, total;
-};
-
-GluLayout glu_layout(const Shape &s, int R, int G) {
-    GluLayout L;
-    L.R = R;
-    L.G = G;
-    L.ldx = s.m1 + 1;
-    L.ldb = L.ldt = G * s.m2 + 1;
-    L.ldc = s.q + 1;
-    size_t o = 0;
-    L.offX = o; o = up4(o + (size_t)R * s.p * L.ldx);
-    L.offB = o; o = up4(o + (size_t)s.m1 * L.ldb);
-    L.offC = o; o = up4(o + (size_t)G * s.p * L.ldc);
-    L.offT = o; o = up4(o + (size_t)R * s.p * L.ldt);
-    L.offG = o; o = up4(o + (size_t)R * s.q * s.m2);
-    L.offU = o; o = up4(o + (size_t)R * s.q * s.m2);
-    L.total = o;
-    return L;
-}
-
-template <bool GRAD>
-__global__ void __launch_bounds__(kThreads)
-kron_glu_simt_kernel(const float *__restrict__ x, const float *__restrict__ S,
-                     const float *__restrict__ A, const float *__restrict__ B,
-                     const float *__restrict__ bias, const float *__restrict__ dH,
-                     float *__restrict__ out0, float *__restrict__ out1, Shape s, GluLayout L,
-                     int act) {
-    extern __shared__ __align__(16) float smem[];
-    float *Xs = smem + L.offX, *Bs = smem + L.offB, *Cs = smem + L.offC, *Ts = smem + L.offT;
-    float *Gs = smem + L.offG, *Us = smem + L.offU;
-    const int R = L.R, P = s.p, Q = s.q, M1 = s.m1, M2 = s.m2;
-    const int64_t n0 = (int64_t)blockIdx.x * R;
-    load_rows(x, n0, s.N, R, P * M1, Xs, M1, L.ldx);
-    for (int f0 = 0; f0 < 2 * s.r; f0 += L.G) {
-        const int f1 = min(f0 + L.G, 2 * s.r);
-        __syncthreads();
-        for (int f = f0; f < f1; ++f)
-            load_factors(S + (f < s.r ? 0 : (size_t)P * Q), A, B, f, s, Bs + (f - f0) * M2, L.ldb,
-                         Cs + (size_t)(f - f0) * P * L.ldc, L.ldc);
-        __syncthreads();
-        // stage 1: T[(n,a),(f,k)] = sum_j X[(n,a),j] B_f[j,k]
-        MM g1{Xs, 0, L.ldx, 0, 1, Bs, 0, 0, L.ldb, 1, Ts, 0, L.ldt, 1, R * P, (f1 - f0) * M2, 1, M1};
-        smem_mm(g1, false);
-        __syncthreads();
-        // stage 2, batched over rows n: Y[(n,c),k] += sum_(f,a) C_f[a,c] T[(n,a),(f,k)]
-        const int gate = max(0, min(f1, s.r) - f0), up = f1 - f0 - gate;
-        MM g2{Cs, 0, 1, P * L.ldc, L.ldc, Ts, P * L.ldt, M2, L.ldt, 1, Gs, Q * M2, M2, R, Q, M2,
-              gate, P};
-        MM g3 = g2;
-        g3.A += (size_t)gate * P * L.ldc;
-        g3.B += gate * M2;
-        g3.C = Us;
-        g3.K1 = up;
-        const int n2 = gate ? mm_items<4, 4>(g2) : 0, n3 = up ? mm_items<4, 4>(g3) : 0;
-        for (int t = threadIdx.x; t < n2 + n3; t += blockDim.x)
-            if (t < n2) mm_item<4, 4>(g2, t, f0 > 0);
-            else mm_item<4, 4>(g3, t - n2, f0 > s.r);
-    }
-    __syncthreads();
-    const int out = Q * M2, o4 = out >> 2;
-    for (int e = threadIdx.x; e < R * o4; e += blockDim.x) {
-        const int n = e / o4, c4 = (e - n * o4) << 2;
-        if (n0 + n >= s.N) continue;
-        const size_t o = (size_t)(n0 + n) * out + c4;
-        float4 g = *reinterpret_cast<const float4 *>(Gs + n * out + c4);
-        float4 u = *reinterpret_cast<const float4 *>(Us + n * out + c4);
-        if (bias != nullptr) {
-            const float4 b0 = load4(bias + c4), b1 = load4(bias + out + c4);
-            g.x += b0.x; g.y += b0.y; g.z += b0.z; g.w += b0.w;
-            u.x += b1.x; u.y += b1.y; u.z += b1.z; u.w += b1.w;
-        }
-        float *pg = &g.x, *pu = &u.x;
-        if constexpr (GRAD) {
-            const float4 h = load4(dH + o);
-            const float *ph = &h.x;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float d;
-                const float f = glu::act_f32(act, pg[t], &d);
-                pg[t] = ph[t] * pu[t] * d;
-                pu[t] = ph[t] * f;
-            }
-            store4(out0 + o, g);
-            store4(out1 + o, u);
-        } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                float d;
-                pu[t] *= glu::act_f32(act, pg[t], &d);
-            }
-            store4(out0 + o, u);
-        }
-    }
-}
-
 template <typename TI>
 __global__ void __launch_bounds__(kThreads)
 kron_bwd_simt_kernel(const TI *__restrict__ x, const TI *__restrict__ S,
@@ -1124,45 +1020,9 @@ cudaError_t simt_backward_t(const void *x, const void *S, const void *A, const v
                               (TI *)nullptr);
 }
 
-// Tile of kron_glu_simt_kernel: the most rows that leave two CTAs on an SM and as many tiles as
-// SMs, with as many terms at a time as fit beside them; else whatever fits at all (R = 0: nothing).
-GluLayout glu_choose(const Shape &s) {
-    for (const size_t limit : {(size_t)113 * 1024, kMaxSmem})
-        for (int R : {8, 4, 2, 1}) {
-            if (R > 1 && (s.N + R - 1) / R < kRowParts) continue;
-            for (int G = 2 * s.r < 8 ? 2 * s.r : 8; G >= 1; --G) {
-                const GluLayout L = glu_layout(s, R, G);
-                if (L.total * sizeof(float) <= limit) return L;
-            }
-        }
-    GluLayout none = glu_layout(s, 1, 1);
-    none.R = 0;
-    return none;
-}
-
 }  // namespace
 
 namespace glu {
-
-bool simt_pre_supported(const Shape &s) { return glu_choose(s).R > 0; }
-
-cudaError_t simt_pre(const void *x, const void *S, const void *A, const void *B, const void *bias,
-                     const void *dH, void *out0, void *out1, const Shape &s, int activation,
-                     bool grad, cudaStream_t st) {
-    const GluLayout L = glu_choose(s);
-    const int R = L.R;
-    const size_t smem = L.total * sizeof(float);
-    auto *f = grad ? kron_glu_simt_kernel<true> : kron_glu_simt_kernel<false>;
-    launch_step() = "shared memory size";
-    cudaError_t e =
-        cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    launch_step() = "gated launch";
-    f<<<(unsigned)((s.N + R - 1) / R), kThreads, smem, st>>>(
-        (const float *)x, (const float *)S, (const float *)A, (const float *)B,
-        (const float *)bias, (const float *)dH, (float *)out0, (float *)out1, s, L, activation);
-    return cudaGetLastError();
-}
 
 cudaError_t simt_backward_pair(const void *x, const void *S, const void *A, const void *B,
                                const void *G0, const void *G1, void *dX0, void *dX1, float *ws,

@@ -373,7 +373,7 @@ def ks_backward(x, w, dY, need_dx=True, need_dbias=True, workspace=None, grads=N
 
 def _need(t, name, dtype, shape, dev):
     """t is a contiguous CUDA tensor of this dtype and shape on device dev."""
-    if (t.dtype is dtype and t.shape == shape and t.is_cuda and t.device == dev
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev.index
             and t.is_contiguous()):
         return
     _expect(t, name, dtype, shape)

@@ -103,7 +103,8 @@ def check_grad(got, ref, size, dtype):
 KW = dict(temperature=1.0, label_weight=0.0)
 MODES = [(1.0, 0.0), (1.0, 0.4), (2.0, 0.3), (4.0, 0.25), (1.5, 0.5), (3.0, 0.0), (2.0, 1.0)]
 # a warp per row (up to 1024 columns and 64 entries) and a CTA per row, on both sides of the edge
-SHAPES = [(13, 1024, 64), (13, 1025, 64), (13, 1024, 65), (2001, 10, 5), (1, 1, 1), (7, 2, 2), (6, 7, 3), (9, 10, 5), (8, 257, 64), (6, 1000, 300),
+SHAPES = [(13, 1024, 64), (13, 1025, 64), (13, 1024, 65), (2001, 10, 5), (1, 1, 1), (7, 2, 2),
+          (6, 7, 3), (9, 10, 5), (8, 257, 64), (6, 1000, 300),
           (7, 4096, 1), (3, 50257, 64)]
 
 

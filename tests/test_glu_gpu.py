@@ -85,7 +85,8 @@ def test_bf16_rows(N, name):
     compare(run(d, name, "bf16"), reference(d, name), "bf16")
 
 
-F32 = [(32, 32, 32, 32, 4, 2500), (128, 128, 8, 8, 2, 19), (64, 64, 64, 64, 2, 5), (4, 4, 4, 4, 1, 3), (9, 11, 12, 20, 3, 37), (32, 32, 32, 32, 4, 65), (1, 1, 4, 4, 1, 1),
+F32 = [(32, 32, 32, 32, 4, 2500), (128, 128, 8, 8, 2, 19), (64, 64, 64, 64, 2, 5),
+       (4, 4, 4, 4, 1, 3), (9, 11, 12, 20, 3, 37), (32, 32, 32, 32, 4, 65), (1, 1, 4, 4, 1, 1),
        (32, 24, 16, 32, 2, 777), (7, 3, 28, 8, 2, 150)]
 
 
@@ -95,6 +96,20 @@ def test_f32(case):
     for k, name in enumerate(ACTS):
         d = make(N, *shape, dtype="f32", seed=k, bias=k != 1)
         compare(run(d, name, "f32"), reference(d, name), "f32")
+
+
+# several passes over the ranks, the last one shorter; several tiles per CTA in each form; a last
+# slice of k that is narrower; more columns c than one kernel takes
+F32_TILES = [(32, 32, 32, 32, 9, 300), (64, 64, 32, 32, 6, 2000), (8, 8, 12, 20, 3, 6000),
+             (40, 33, 28, 44, 5, 1200), (3, 70, 8, 100, 2, 33), (2, 2100, 4, 4, 1, 5)]
+
+
+@pytest.mark.parametrize("case", F32_TILES, ids=lambda s: "p{}q{}_m{}x{}_r{}_N{}".format(*s))
+def test_f32_passes_and_tiles(case):
+    *shape, N = case
+    d = make(N, *shape, dtype="f32", seed=N)
+    name = ACTS[N % 4]
+    compare(run(d, name, "f32"), reference(d, name), "f32")
 
 
 def test_many_rows():
