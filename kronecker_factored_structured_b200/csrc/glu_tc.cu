@@ -14,8 +14,9 @@
 // (12 warps) moves a chunk TMEM -> bf16 -> shared memory, which is the permute of the vec trick;
 // epilogue 2 (16 warps) has g and u of one (n, k, c) side by side.  For kInput the kernel runs
 // with transposed factors, dg against the gate's and du against the up's ranks, and the two
-// accumulators are added.  T is rounded to BF16 between the stages, as in the layer's own
-// kernels: half a step, 2^-8 of each term.
+// accumulators are added.  T is rounded to BF16 between the stages and C_i = S (.) A_i as it is
+// packed, as in the layer's own kernels, because the MMA takes BF16 operands: each half a step,
+// 2^-8 of a term.
 //
 // A CTA holds the factors of one (k slice, c slice) in shared memory for its life and streams
 // row tiles; slices exist where the factors do not fit at once, and for few rows, where the
