@@ -306,8 +306,9 @@ kron_status_t kron_glu_backward(const void *x, const void *S, const void *A, con
     }
     float *g = (float *)ws, *u = (float *)(ws + hb), *dx2 = (float *)(ws + 2 * hb);
     float *part = (float *)(ws + 2 * hb + pad256((size_t)N * din * 4));
-    const int parts = (int)(kron_linear_workspace_size(N, p, q, m1, m2, r, KRON_F32) /
-                            (partial_stride(s) * sizeof(float)));
+    const int max_parts = (int)(kron_linear_workspace_size(N, p, q, m1, m2, r, KRON_F32) /
+                                (partial_stride(s) * sizeof(float)));
+    int parts = max_parts;
     if (fused_f32(s)) {
         e = glu::f32_pre(x, S, A, B, bias, dH, g, u, s, activation, true, cs);
     } else {
@@ -321,7 +322,8 @@ kron_status_t kron_glu_backward(const void *x, const void *S, const void *A, con
         }
     }
     if (e == cudaSuccess)
-        e = glu::simt_backward_pair(x, S, A, B, g, u, dX, dX ? dx2 : nullptr, part, parts, s, cs);
+        e = glu::f32_backward_pair(x, S, A, B, g, u, dX, dX ? dx2 : nullptr, part, max_parts,
+                                   &parts, s, cs);
     if (e == cudaSuccess)
         e = glu::reduce_partials_pair(part, parts, S, A, (float *)dS, (float *)dA, (float *)dB,
                                       (float *)dbias, s, cs);

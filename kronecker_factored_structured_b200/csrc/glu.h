@@ -48,6 +48,10 @@ cudaError_t f32_pre(const void *x, const void *S, const void *A, const void *B, 
 cudaError_t simt_backward_pair(const void *x, const void *S, const void *A, const void *B,
                                const void *G0, const void *G1, void *dX0, void *dX1, float *ws,
                                int parts, const Shape &s, cudaStream_t st);
+// The same by a kernel of its own where its tiles fit; the partials of `parts` <= max_parts ranges.
+cudaError_t f32_backward_pair(const void *x, const void *S, const void *A, const void *B,
+                              const void *G0, const void *G1, void *dX0, void *dX1, float *ws,
+                              int max_parts, int *parts, const Shape &s, cudaStream_t st);
 // reduce_partials of both projections; gradients stacked as the factors are (reduce.cu).
 cudaError_t reduce_partials_pair(const float *ws, int parts, const void *S, const void *A,
                                  float *dS, float *dA, float *dB, float *dbias, const Shape &s,

@@ -324,6 +324,296 @@ bool find_plan(FPlan *best, const Shape &s) {
     return found;
 }
 
+// ---- backward of both projections ----
+//
+// A CTA takes a range of rows of one projection, in tiles of R rows, all ranks at once (G = dg or
+// du):
+//   U[(n,a),(i,k)] = sum_c C_i[a,c] G[(n,c),k]        T[(n,a),(i,k)] = sum_j X[(n,a),j] B_i[j,k]
+//   dX[(n,a),j] = sum_(i,k) U B_i[j,k]   dB_i[j,k] += sum_(n,a) X U   dC_i[a,c] += sum_(n,k) T G
+// Each tensor lies once in shared memory; 8 x 8 outputs per thread take a step of four summed
+// indices by 16 loads of four words whichever way an operand lies.  dB and dC have few outputs and
+// a long sum, so `slots` sets of them are summed side by side, each over its rows of the tile, and
+// added in order at the end: bitwise reproducible.  777 rows, 512 -> 768, r = 2: 42 us (the
+// layer's own kernel, 4 x 4 outputs and one rank at a time: 75); whole backward calls of 1 to 20000
+// rows and blocks of 8 to 100 take 0.6 to 1.0 of the time that they took with that kernel.
+struct BPlan {
+    int R, slots, parts;
+    int64_t rows;                  // per range
+    int Pp, Qp, ldx, ldg, ldc, ldt;
+    int offG, offB, offC, offU, offT, offS, offD, smem;    // words; smem in bytes
+};
+
+struct Operand {
+    const float *p;
+    int s, t;       // summed index innermost: rows s apart; else: s between summed indices, the
+};                  // second four outputs t behind the first
+
+__device__ __forceinline__ float part(const float4 &v, int w) {
+    return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+}
+
+template <bool AI, bool BI>
+__device__ __forceinline__ void mm8(float (&acc)[8][8], const Operand &a, const Operand &b, int K) {
+    static_assert(AI || !BI, "not needed");
+#pragma unroll 1
+    for (int k = 0; k < K; k += 4) {
+        float4 av[8];
+        if constexpr (AI) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) av[u] = four(a.p + u * a.s + k);
+        }
+        if constexpr (BI) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v) {
+                const float4 bv = four(b.p + v * b.s + k);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) acc[u][v] = dot4(av[u], bv, acc[u][v]);
+            }
+        } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 b0 = four(b.p + (k + w) * b.s), b1 = four(b.p + (k + w) * b.s + b.t);
+                float4 a0, a1;
+                if constexpr (!AI) a0 = four(a.p + (k + w) * a.s), a1 = four(a.p + (k + w) * a.s + a.t);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    float f;
+                    if constexpr (AI) f = part(av[u], w);
+                    else f = u < 4 ? part(a0, u) : part(a1, u - 4);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        acc[u][v] = fmaf(f, part(b0, v), acc[u][v]);
+                        acc[u][v + 4] = fmaf(f, part(b1, v), acc[u][v + 4]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ int eighth(int n) { return (n + 7) >> 3; }
+__device__ __forceinline__ int warps_of(int n) { return (n + 31) & ~31; }
+
+__global__ void __launch_bounds__(kThreads, 1)
+glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S,
+                        const float *__restrict__ A, const float *__restrict__ B,
+                        const float *__restrict__ g0, const float *__restrict__ g1,
+                        float *__restrict__ dx0, float *__restrict__ dx1, float *__restrict__ ws,
+                        const size_t ws_stride, const Shape s, const BPlan pl) {
+    extern __shared__ __align__(16) float smem[];
+    float *const Xs = smem, *const Gs = smem + pl.offG, *const Bs = smem + pl.offB;
+    float *const Cs = smem + pl.offC, *const Us = smem + pl.offU, *const Ts = smem + pl.offT;
+    float *const Ss = smem + pl.offS, *const Ds = smem + pl.offD;      // slots of dC and dB, dbias
+    const int P = s.p, Q = s.q, M1 = s.m1, M2 = s.m2, r = s.r, R = pl.R, rk = r * M2;
+    const int Pp = pl.Pp, Qp = pl.Qp, ldx = pl.ldx, ldg = pl.ldg, ldc = pl.ldc, ldt = pl.ldt;
+    const int proj = blockIdx.y, n_dc = r * P * Q, n_db = r * M1 * M2;
+    S += (size_t)proj * P * Q;
+    A += (size_t)proj * n_dc;
+    B += (size_t)proj * n_db;
+    const float *const G = proj ? g1 : g0;
+    float *const dX = proj ? dx1 : dx0;
+    float *const out = ws + ((size_t)proj * gridDim.x + blockIdx.x) * ws_stride;
+    const int64_t lo = blockIdx.x * pl.rows, hi = lo + pl.rows < s.N ? lo + pl.rows : s.N;
+
+    for (int e = threadIdx.x; e < pl.slots * (n_dc + n_db); e += kThreads) Ss[e] = 0.f;
+    for (int e = threadIdx.x; e < Q * M2; e += kThreads) Ds[e] = 0.f;
+    for (int e = threadIdx.x; e < r * M1 * (M2 >> 2); e += kThreads) {    // B as [j][(i,k)]
+        const int row = e / (M2 >> 2), k = (e - row * (M2 >> 2)) << 2, i = row / M1;
+        copy16(Bs + (row - i * M1) * ldt + i * M2 + k, B + (size_t)row * M2 + k, true);
+    }
+    for (int e = threadIdx.x; e < r * Pp * Qp; e += kThreads) {           // C as [i][a][c]
+        const int row = e / Qp, c = e - row * Qp, i = row / Pp, a = row - i * Pp;
+        float v = 0.f;
+        if (a < P && c < Q) v = S[(size_t)a * Q + c] * A[((size_t)i * P + a) * Q + c];
+        Cs[row * ldc + c] = v;
+    }
+    const int MT = eighth(P), NT = eighth(M2), CT = eighth(Q), JT = eighth(M1);
+    const int MR = eighth(R * Pp), nq = M2 >> 2, jq = M1 >> 2;
+    const int n_ut = R * r * MT * NT;
+    const int n_x = dX ? warps_of(MR * JT) : 0, n_c = warps_of(pl.slots * r * MT * CT);
+    const int n_b = warps_of(pl.slots * r * JT * NT);
+    for (int64_t n0 = lo; n0 < hi; n0 += R) {
+        for (int e = threadIdx.x; e < R * Pp * jq; e += kThreads) {
+            const int row = e / jq, j = (e - row * jq) << 2, n = row / Pp, a = row - n * Pp;
+            const bool live = a < P && n0 + n < hi;
+            copy16(Xs + row * ldx + j, live ? x + ((n0 + n) * P + a) * M1 + j : x, live);
+        }
+        for (int e = threadIdx.x; e < R * Qp * nq; e += kThreads) {
+            const int row = e / nq, k = (e - row * nq) << 2, n = row / Qp, c = row - n * Qp;
+            const bool live = c < Q && n0 + n < hi;
+            copy16(Gs + row * ldg + k, live ? G + ((n0 + n) * Q + c) * M2 + k : G, live);
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        for (int t = threadIdx.x; t < 2 * n_ut; t += kThreads) {
+            const bool second = t >= n_ut;           // T
+            int e = second ? t - n_ut : t;
+            const int tk = e % NT;
+            e /= NT;
+            const int ta = e % MT;
+            e /= MT;
+            const int i = e % r, n = e / r;
+            Operand oa, ob;
+            if (second) {
+                oa = Operand{Xs + (n * Pp + ta) * ldx, MT * ldx, 0};
+                ob = Operand{Bs + i * M2 + 4 * tk, ldt, 4 * NT};
+            } else {
+                oa = Operand{Cs + (i * Pp + ta) * ldc, MT * ldc, 0};
+                ob = Operand{Gs + n * Qp * ldg + 4 * tk, ldg, 4 * NT};
+            }
+            float acc[8][8] = {};
+            mm8<true, false>(acc, oa, ob, second ? M1 : Qp);
+            float *d = (second ? Ts : Us) + n * Pp * ldt + i * M2 + 4 * tk;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int a = ta + u * MT;
+                if (a >= Pp) break;
+                const bool live = a < P;       // zero behind the last a, also for infinite factors
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (tk + h * NT < nq)
+                        *reinterpret_cast<float4 *>(d + a * ldt + 4 * h * NT) =
+                            live ? make_float4(acc[u][4 * h], acc[u][4 * h + 1], acc[u][4 * h + 2],
+                                               acc[u][4 * h + 3])
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+        __syncthreads();
+        for (int t = threadIdx.x; t < n_x + n_c + n_b; t += kThreads) {
+            float acc[8][8] = {};
+            if (t < n_x + n_c) {
+                const bool is_x = t < n_x;
+                int e = is_x ? t : t - n_x;
+                int n = 0, step = R, K = rk, i = 0, ta, tb;
+                Operand oa, ob;
+                if (is_x) {
+                    tb = e % JT;
+                    ta = e / JT;
+                    if (ta >= MR) continue;
+                    oa = Operand{Us + ta * ldt, MR * ldt, 0};
+                    ob = Operand{Bs + tb * ldt, JT * ldt, 0};
+                } else {
+                    tb = e % CT;
+                    e /= CT;
+                    ta = e % MT;
+                    e /= MT;
+                    i = e % r;
+                    n = e / r;
+                    if (n >= pl.slots) continue;
+                    step = pl.slots;
+                    K = M2;
+                    oa = Operand{Ts + (n * Pp + ta) * ldt + i * M2, MT * ldt, 0};
+                    ob = Operand{Gs + (n * Qp + tb) * ldg, CT * ldg, 0};
+                }
+                const int slot = n;
+                for (; n < R; n += step) {
+                    mm8<true, true>(acc, oa, ob, K);
+                    oa.p += step * Pp * ldt;
+                    ob.p += step * Qp * ldg;
+                }
+                if (is_x) {
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        const int row = ta + u * MR, rn = row / Pp, a = row - rn * Pp;
+                        if (rn >= R || a >= P || n0 + rn >= hi) continue;
+                        float *d = dX + ((n0 + rn) * P + a) * M1;
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            if (tb + v * JT < M1) d[tb + v * JT] = acc[u][v];
+                    }
+                } else {
+                    float *d = Ss + slot * (n_dc + n_db) + i * P * Q;
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+#pragma unroll
+                        for (int v = 0; v < 8; ++v)
+                            if (ta + u * MT < P && tb + v * CT < Q)
+                                d[(ta + u * MT) * Q + tb + v * CT] += acc[u][v];
+                }
+            } else {
+                int e = t - n_x - n_c;
+                const int tk = e % NT;
+                e /= NT;
+                const int tj = e % JT;
+                e /= JT;
+                const int i = e % r, slot = e / r;
+                if (slot >= pl.slots) continue;
+                for (int n = slot; n < R; n += pl.slots)
+                    mm8<false, false>(acc, Operand{Xs + n * Pp * ldx + 4 * tj, ldx, 4 * JT},
+                                      Operand{Us + n * Pp * ldt + i * M2 + 4 * tk, ldt, 4 * NT}, Pp);
+                float *d = Ss + slot * (n_dc + n_db) + n_dc + (size_t)i * M1 * M2;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int j = 4 * (tj + (u >> 2) * JT) + (u & 3);
+                    if (j >= M1) break;
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        if (tk + (v >> 2) * NT < nq)
+                            d[j * M2 + 4 * (tk + (v >> 2) * NT) + (v & 3)] += acc[u][v];
+                }
+            }
+        }
+        for (int e = threadIdx.x; e < Q * M2; e += kThreads) {
+            const int c = e / M2, k = e - c * M2;
+            float v = 0.f;
+            for (int n = 0; n < R; ++n) v += Gs[(n * Qp + c) * ldg + k];
+            Ds[e] += v;
+        }
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < n_dc + n_db; e += kThreads) {
+        float v = 0.f;
+        for (int k = 0; k < pl.slots; ++k) v += Ss[k * (n_dc + n_db) + e];
+        out[e] = v;
+    }
+    for (int e = threadIdx.x; e < Q * M2; e += kThreads) out[n_dc + n_db + e] = Ds[e];
+}
+
+// Ranges for one CTA per SM; the largest tile that fits shared memory, then as many slots.  At
+// least two rows per tile, or all of the range.
+bool backward_plan(BPlan *b, const Shape &s, int max_parts) {
+    BPlan p{};
+    int parts = kRowParts / 2 < max_parts ? kRowParts / 2 : max_parts;
+    p.rows = (s.N + parts - 1) / parts;
+    p.parts = cdiv(s.N, p.rows);
+    p.Pp = up4i(s.p);
+    p.Qp = up4i(s.q);
+    p.ldx = odd4(s.m1);
+    p.ldg = odd4(s.m2);
+    p.ldc = odd4(p.Qp);
+    const int64_t rk = (int64_t)s.r * s.m2;
+    if (rk > 4096 || s.d_out() > 16384 || s.p > 1024 || (int64_t)s.r * s.p * s.q > 16384 ||
+        rk * s.m1 > 16384)
+        return false;
+    p.ldt = odd4((int)rk);
+    const int sums = (int)((int64_t)s.r * s.p * s.q + rk * s.m1);
+    // the last rows of a tensor are read up to seven rows further
+    const int ld = p.ldt > p.ldc ? p.ldt : p.ldc, ld2 = p.ldx > p.ldg ? p.ldx : p.ldg;
+    const int tail = 8 * (ld > ld2 ? ld : ld2);
+    const int most = (int)(p.rows < 16 ? p.rows : 16);
+    for (int R = most; R >= 1 && (R > 1 || p.rows == 1); --R) {
+        const int tiles = cdiv(p.rows, R);
+        if (cdiv(p.rows, tiles) != R && R != most) continue;       // tiles of equal height
+        p.R = R;
+        p.offG = R * p.Pp * p.ldx;
+        p.offB = p.offG + R * p.Qp * p.ldg;
+        p.offC = p.offB + s.m1 * p.ldt;
+        p.offU = p.offC + s.r * p.Pp * p.ldc;
+        p.offT = p.offU + R * p.Pp * p.ldt;
+        p.offS = p.offT + R * p.Pp * p.ldt;
+        for (int slots = R; slots >= 1; --slots) {
+            p.slots = slots;
+            p.offD = p.offS + up4i(slots * sums);
+            const int64_t words = p.offD + s.d_out() + tail;
+            if (words * 4 > kMaxSmem) continue;
+            p.smem = (int)words * 4;
+            *b = p;
+            return true;
+        }
+    }
+    return false;
+}
+
 }  // namespace
 
 // A call needs the plan twice: the last one is kept.
@@ -359,6 +649,30 @@ cudaError_t f32_pre(const void *x, const void *S, const void *A, const void *B, 
     f<<<dim3((unsigned)p.grid, (unsigned)p.nks), kThreads, p.smem, st>>>(
         (const float *)x, (const float *)S, (const float *)A, (const float *)B,
         (const float *)bias, (const float *)dH, (float *)out0, (float *)out1, s, p, activation);
+    return cudaGetLastError();
+}
+
+cudaError_t f32_backward_pair(const void *x, const void *S, const void *A, const void *B,
+                              const void *G0, const void *G1, void *dX0, void *dX1, float *ws,
+                              int max_parts, int *parts, const Shape &s, cudaStream_t st) {
+    BPlan p;
+    // the compiled shape has kernels of its own, faster where rows are many: 1024 rows 208 us here
+    // for the whole backward call and 211 there, 2368 rows 400 and 357, 20000 rows 2922 and 2278
+    const bool own = s.p == 32 && s.q == 32 && s.m1 == 32 && s.m2 == 32 && s.r == 4 &&
+                     s.N >= 10 * kRowParts;
+    if (own || !backward_plan(&p, s, max_parts)) {
+        *parts = max_parts;
+        return simt_backward_pair(x, S, A, B, G0, G1, dX0, dX1, ws, max_parts, s, st);
+    }
+    *parts = p.parts;
+    launch_step() = "shared memory size";
+    cudaError_t e = cudaFuncSetAttribute(glu_f32_backward_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    if (e != cudaSuccess) return e;
+    launch_step() = "backward launch";
+    glu_f32_backward_kernel<<<dim3((unsigned)p.parts, 2), kThreads, p.smem, st>>>(
+        (const float *)x, (const float *)S, (const float *)A, (const float *)B, (const float *)G0,
+        (const float *)G1, (float *)dX0, (float *)dX1, ws, partial_stride(s), s, p);
     return cudaGetLastError();
 }
 
