@@ -131,12 +131,12 @@ kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int ac
 }
 
 // F32: whether both projections run in one kernel with the activation.  The compiled shape's own
-// kernels are faster than that one where they have rows to fill the SMs with: forward of 1024 rows
-// 57 us in one kernel and 73 in two and an elementwise pass, 2368 rows 139 and 105, 20000 rows 913
-// and 613; backward 211 and 226, 395 and 357, 2608 and 2278.
+// kernels are faster than that one where they have rows to fill the SMs with: forward of 2000 rows
+// 90 us in one kernel and 101 in two and an elementwise pass, 2368 rows 117 and 103, 20000 rows
+// 766 and 616.
 bool fused_f32(const Shape &s) {
     const bool compiled = s.p == 32 && s.q == 32 && s.m1 == 32 && s.m2 == 32 && s.r == 4;
-    return glu::f32_pre_supported(s) && !(compiled && s.N >= 10 * kRowParts);
+    return glu::f32_pre_supported(s) && !(compiled && s.N >= glu::kCompiledRows);
 }
 
 // Workspace: forward F32 [g] unless fused; backward F32 [g][u][dX of up][partials of both];

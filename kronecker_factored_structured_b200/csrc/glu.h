@@ -37,6 +37,9 @@ struct Plan {
 };
 
 // ---- exact FP32 (glu_f32.cu, simt_f32.cu) ----
+// Rows from which on the layer's kernels for its compiled shape (p = q = m1 = m2 = 32, r = 4) are
+// the faster ones.
+constexpr int64_t kCompiledRows = 15 * kRowParts;
 // Whether both projections, the activation and the product of this shape run as one kernel.
 bool f32_pre_supported(const Shape &s);
 // h (grad = false), or dg and du from dH (grad = true); factors stacked gate, up.

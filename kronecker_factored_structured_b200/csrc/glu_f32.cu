@@ -10,11 +10,12 @@
 // gate's and half the up projection's; the sums meet in shared memory, for the whole CTA to apply
 // the activation to.  Row strides are 4 mod 8 words: neighbouring threads read neighbouring rows,
 // on distinct banks.
-// 1000 x 1024, r = 2: 28 us (4 x 4 outputs, one word per load, two CTAs of 4 rows per SM: 45;
-// packed multiply-adds over pairs of the summed index, 4 x 8 outputs: 28, but 1.6 times the time
-// at 20000 rows: one takes 2.3 cycles, two plain ones the same).  FFMA bounds it from below: a
-// stage takes 15,500 cycles, 8,200 of FFMA and 7,200 of shared memory, one after the other, as
-// the warps load in step; loads one step ahead need more registers than there are (26,000).
+// FFMA bounds it from below, 8,200 cycles per stage for 1000 x 1024, r = 2, and then the loads,
+// 7,200: a warp's step takes both in turn unless the next step's loads run while it computes,
+// which takes the registers of 256 threads.  That size takes 28 us, with the loads of the factors
+// and the packing of rows into tiles (4 x 4 outputs, one word per load, two CTAs of 4 rows per SM:
+// 45); 20000 rows 357 us, 30 TFLOP/s (512 threads, no loads ahead: 416).  Packed multiply-adds
+// over pairs of the summed index were no faster: one takes 2.3 cycles, two plain ones the same.
 #include "glu.h"
 #include "internal.h"
 
@@ -22,7 +23,7 @@ namespace kron {
 namespace glu {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256, kBackThreads = 384;
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kHalf = kThreads / 2;    // stage-2 items
 
@@ -50,8 +51,69 @@ inline int odd4(int v) { return (up4i(v) & 4) ? up4i(v) : up4i(v) + 4; }
 __device__ __forceinline__ float4 four(const float *p) {
     return *reinterpret_cast<const float4 *>(p);
 }
-__device__ __forceinline__ float dot4(const float4 &a, const float4 &b, float c) {
-    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+struct Operand {
+    const float *p;
+    int s, t;       // summed index innermost: four rows s apart, the second four t behind them;
+};                  // else: s between summed indices, the second four outputs t behind the first
+
+__device__ __forceinline__ float part(const float4 &v, int w) {
+    return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ void rows8(float4 (&v)[8], const Operand &a, int k) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = four(a.p + (u & 3) * a.s + (u >> 2) * a.t + k);
+}
+
+// acc += a b over K values, a multiple of 4; AI, BI: whether the summed index lies innermost;
+// AHEAD: whether a step's rows of a are loaded while the one before computes (forward: 3000 rows,
+// r = 3, 115 us instead of 141; backward, which lacks the registers: 368 instead of 357).
+template <bool AI, bool BI, bool AHEAD>
+__device__ __forceinline__ void mm8(float (&acc)[8][8], const Operand &a, const Operand &b, int K) {
+    static_assert(AI || !BI, "not needed");
+    float4 av[8];
+    if constexpr (AI && AHEAD) rows8(av, a, 0);
+#pragma unroll 1
+    for (int k = 0; k < K; k += 4) {
+        float4 next[8];
+        if constexpr (AI && !AHEAD) rows8(av, a, k);
+        if constexpr (AI && AHEAD) rows8(next, a, min(k + 4, K - 4));
+        if constexpr (BI) {
+            float4 bv[8];
+            rows8(bv, b, k);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        acc[u][v] = fmaf(part(av[u], w), part(bv[v], w), acc[u][v]);
+        } else {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float4 b0 = four(b.p + (k + w) * b.s), b1 = four(b.p + (k + w) * b.s + b.t);
+                float4 a0, a1;
+                if constexpr (!AI) {
+                    a0 = four(a.p + (k + w) * a.s);
+                    a1 = four(a.p + (k + w) * a.s + a.t);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    float f;
+                    if constexpr (AI) f = part(av[u], w);
+                    else f = u < 4 ? part(a0, u) : part(a1, u - 4);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        acc[u][v] = fmaf(f, part(b0, v), acc[u][v]);
+                        acc[u][v + 4] = fmaf(f, part(b1, v), acc[u][v + 4]);
+                    }
+                }
+            }
+        }
+        if constexpr (AI && AHEAD) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) av[u] = next[u];
+        }
+    }
 }
 
 __device__ __forceinline__ void copy16(float *dst, const float *src, bool live) {
@@ -150,18 +212,8 @@ glu_f32_kernel(const float *__restrict__ x, const float *__restrict__ S,
                 for (int u = 0; u < 8; ++u)
 #pragma unroll
                     for (int v = 0; v < 8; ++v) acc[u][v] = 0.f;
-#pragma unroll 1
-                for (int j = 0; j < M1; j += 4) {
-                    float4 xv[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) xv[u] = four(px + u * MT * ldx + j);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        const float4 b = four(pb + v * NT * ldx + j);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) acc[u][v] = dot4(xv[u], b, acc[u][v]);
-                    }
-                }
+                mm8<true, true, true>(acc, Operand{px, MT * ldx, 4 * MT * ldx},
+                                Operand{pb, NT * ldx, 4 * NT * ldx}, M1);
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const int rn = over(tm * 8 + 4 * g, pl.d_pp), a = tm * 8 + 4 * g - rn * Pp;
@@ -188,23 +240,9 @@ glu_f32_kernel(const float *__restrict__ x, const float *__restrict__ S,
                 for (int i = 0; i < gl; ++i) {
                     const float *pt = Ts + (n * NC + (h * G + i) * KS + tk) * lda;
                     const float *pc = Cs + ((h * G + i) * Q + tc) * lda;
-                    const int second = (tk1 - tk) * lda;
-#pragma unroll 1
-                    for (int a = 0; a < Pp; a += 4) {
-                        float4 tv[8];
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            tv[v] = four(pt + v * k4s * lda + a);
-                            tv[v + 4] = four(pt + v * k4s * lda + a + second);
-                        }
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            // columns behind the last c read what is there, for nothing
-                            const float4 c = four(pc + u * CT * lda + a);
-#pragma unroll
-                            for (int v = 0; v < 8; ++v) y[u][v] = dot4(tv[v], c, y[u][v]);
-                        }
-                    }
+                    // columns behind the last c read what is there, for nothing
+                    mm8<true, true, true>(y, Operand{pc, CT * lda, 4 * CT * lda},
+                                    Operand{pt, k4s * lda, (tk1 - tk) * lda}, Pp);
                 }
             }
         }
@@ -333,9 +371,10 @@ bool find_plan(FPlan *best, const Shape &s) {
 // Each tensor lies once in shared memory; 8 x 8 outputs per thread take a step of four summed
 // indices by 16 loads of four words whichever way an operand lies.  dB and dC have few outputs and
 // a long sum, so `slots` sets of them are summed side by side, each over its rows of the tile, and
-// added in order at the end: bitwise reproducible.  777 rows, 512 -> 768, r = 2: 42 us (the
+// added in order at the end: bitwise reproducible.  777 rows, 512 -> 768, r = 2: 38 us (the
 // layer's own kernel, 4 x 4 outputs and one rank at a time: 75); whole backward calls of 1 to 20000
-// rows and blocks of 8 to 100 take 0.6 to 1.0 of the time that they took with that kernel.
+// rows and blocks of 8 to 100 take 0.55 to 1.0 of the time that they took with that kernel.  384
+// threads: 3000 rows, r = 3 take 357 us, with 512 370.
 struct BPlan {
     int R, slots, parts;
     int64_t rows;                  // per range
@@ -343,58 +382,21 @@ struct BPlan {
     int offG, offB, offC, offU, offT, offS, offD, smem;    // words; smem in bytes
 };
 
-struct Operand {
-    const float *p;
-    int s, t;       // summed index innermost: rows s apart; else: s between summed indices, the
-};                  // second four outputs t behind the first
-
-__device__ __forceinline__ float part(const float4 &v, int w) {
-    return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w;
-}
-
-template <bool AI, bool BI>
-__device__ __forceinline__ void mm8(float (&acc)[8][8], const Operand &a, const Operand &b, int K) {
-    static_assert(AI || !BI, "not needed");
-#pragma unroll 1
-    for (int k = 0; k < K; k += 4) {
-        float4 av[8];
-        if constexpr (AI) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u) av[u] = four(a.p + u * a.s + k);
-        }
-        if constexpr (BI) {
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                const float4 bv = four(b.p + v * b.s + k);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) acc[u][v] = dot4(av[u], bv, acc[u][v]);
-            }
-        } else {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float4 b0 = four(b.p + (k + w) * b.s), b1 = four(b.p + (k + w) * b.s + b.t);
-                float4 a0, a1;
-                if constexpr (!AI) a0 = four(a.p + (k + w) * a.s), a1 = four(a.p + (k + w) * a.s + a.t);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    float f;
-                    if constexpr (AI) f = part(av[u], w);
-                    else f = u < 4 ? part(a0, u) : part(a1, u - 4);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        acc[u][v] = fmaf(f, part(b0, v), acc[u][v]);
-                        acc[u][v + 4] = fmaf(f, part(b1, v), acc[u][v + 4]);
-                    }
-                }
-            }
-        }
-    }
+// Four sums of a slot: set by the first tile, added to by the others.
+__device__ __forceinline__ void add4(float *d, const float *acc, bool first) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!first) v = four(d);
+    v.x += acc[0];
+    v.y += acc[1];
+    v.z += acc[2];
+    v.w += acc[3];
+    *reinterpret_cast<float4 *>(d) = v;
 }
 
 __device__ __forceinline__ int eighth(int n) { return (n + 7) >> 3; }
 __device__ __forceinline__ int warps_of(int n) { return (n + 31) & ~31; }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kBackThreads, 1)
 glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S,
                         const float *__restrict__ A, const float *__restrict__ B,
                         const float *__restrict__ g0, const float *__restrict__ g1,
@@ -403,10 +405,12 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
     extern __shared__ __align__(16) float smem[];
     float *const Xs = smem, *const Gs = smem + pl.offG, *const Bs = smem + pl.offB;
     float *const Cs = smem + pl.offC, *const Us = smem + pl.offU, *const Ts = smem + pl.offT;
-    float *const Ss = smem + pl.offS, *const Ds = smem + pl.offD;      // slots of dC and dB, dbias
+    // slots of [dB][dC as [i][a][Qp]], and dbias
+    float *const Ss = smem + pl.offS, *const Ds = smem + pl.offD;
     const int P = s.p, Q = s.q, M1 = s.m1, M2 = s.m2, r = s.r, R = pl.R, rk = r * M2;
     const int Pp = pl.Pp, Qp = pl.Qp, ldx = pl.ldx, ldg = pl.ldg, ldc = pl.ldc, ldt = pl.ldt;
     const int proj = blockIdx.y, n_dc = r * P * Q, n_db = r * M1 * M2;
+    const int n_slot = n_db + r * P * Qp;
     S += (size_t)proj * P * Q;
     A += (size_t)proj * n_dc;
     B += (size_t)proj * n_db;
@@ -415,13 +419,11 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
     float *const out = ws + ((size_t)proj * gridDim.x + blockIdx.x) * ws_stride;
     const int64_t lo = blockIdx.x * pl.rows, hi = lo + pl.rows < s.N ? lo + pl.rows : s.N;
 
-    for (int e = threadIdx.x; e < pl.slots * (n_dc + n_db); e += kThreads) Ss[e] = 0.f;
-    for (int e = threadIdx.x; e < Q * M2; e += kThreads) Ds[e] = 0.f;
-    for (int e = threadIdx.x; e < r * M1 * (M2 >> 2); e += kThreads) {    // B as [j][(i,k)]
+    for (int e = threadIdx.x; e < r * M1 * (M2 >> 2); e += kBackThreads) {    // B as [j][(i,k)]
         const int row = e / (M2 >> 2), k = (e - row * (M2 >> 2)) << 2, i = row / M1;
         copy16(Bs + (row - i * M1) * ldt + i * M2 + k, B + (size_t)row * M2 + k, true);
     }
-    for (int e = threadIdx.x; e < r * Pp * Qp; e += kThreads) {           // C as [i][a][c]
+    for (int e = threadIdx.x; e < r * Pp * Qp; e += kBackThreads) {           // C as [i][a][c]
         const int row = e / Qp, c = e - row * Qp, i = row / Pp, a = row - i * Pp;
         float v = 0.f;
         if (a < P && c < Q) v = S[(size_t)a * Q + c] * A[((size_t)i * P + a) * Q + c];
@@ -433,19 +435,20 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
     const int n_x = dX ? warps_of(MR * JT) : 0, n_c = warps_of(pl.slots * r * MT * CT);
     const int n_b = warps_of(pl.slots * r * JT * NT);
     for (int64_t n0 = lo; n0 < hi; n0 += R) {
-        for (int e = threadIdx.x; e < R * Pp * jq; e += kThreads) {
+        const bool first = n0 == lo;
+        for (int e = threadIdx.x; e < R * Pp * jq; e += kBackThreads) {
             const int row = e / jq, j = (e - row * jq) << 2, n = row / Pp, a = row - n * Pp;
             const bool live = a < P && n0 + n < hi;
             copy16(Xs + row * ldx + j, live ? x + ((n0 + n) * P + a) * M1 + j : x, live);
         }
-        for (int e = threadIdx.x; e < R * Qp * nq; e += kThreads) {
+        for (int e = threadIdx.x; e < R * Qp * nq; e += kBackThreads) {
             const int row = e / nq, k = (e - row * nq) << 2, n = row / Qp, c = row - n * Qp;
             const bool live = c < Q && n0 + n < hi;
             copy16(Gs + row * ldg + k, live ? G + ((n0 + n) * Q + c) * M2 + k : G, live);
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         __syncthreads();
-        for (int t = threadIdx.x; t < 2 * n_ut; t += kThreads) {
+        for (int t = threadIdx.x; t < 2 * n_ut; t += kBackThreads) {
             const bool second = t >= n_ut;           // T
             int e = second ? t - n_ut : t;
             const int tk = e % NT;
@@ -455,14 +458,14 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
             const int i = e % r, n = e / r;
             Operand oa, ob;
             if (second) {
-                oa = Operand{Xs + (n * Pp + ta) * ldx, MT * ldx, 0};
+                oa = Operand{Xs + (n * Pp + ta) * ldx, MT * ldx, 4 * MT * ldx};
                 ob = Operand{Bs + i * M2 + 4 * tk, ldt, 4 * NT};
             } else {
-                oa = Operand{Cs + (i * Pp + ta) * ldc, MT * ldc, 0};
+                oa = Operand{Cs + (i * Pp + ta) * ldc, MT * ldc, 4 * MT * ldc};
                 ob = Operand{Gs + n * Qp * ldg + 4 * tk, ldg, 4 * NT};
             }
             float acc[8][8] = {};
-            mm8<true, false>(acc, oa, ob, second ? M1 : Qp);
+            mm8<true, false, false>(acc, oa, ob, second ? M1 : Qp);
             float *d = (second ? Ts : Us) + n * Pp * ldt + i * M2 + 4 * tk;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -479,7 +482,7 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
             }
         }
         __syncthreads();
-        for (int t = threadIdx.x; t < n_x + n_c + n_b; t += kThreads) {
+        for (int t = threadIdx.x; t < n_x + n_c + n_b; t += kBackThreads) {
             float acc[8][8] = {};
             if (t < n_x + n_c) {
                 const bool is_x = t < n_x;
@@ -490,8 +493,8 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
                     tb = e % JT;
                     ta = e / JT;
                     if (ta >= MR) continue;
-                    oa = Operand{Us + ta * ldt, MR * ldt, 0};
-                    ob = Operand{Bs + tb * ldt, JT * ldt, 0};
+                    oa = Operand{Us + ta * ldt, MR * ldt, 4 * MR * ldt};
+                    ob = Operand{Bs + 4 * tb * ldt, ldt, 4 * JT * ldt};
                 } else {
                     tb = e % CT;
                     e /= CT;
@@ -502,12 +505,12 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
                     if (n >= pl.slots) continue;
                     step = pl.slots;
                     K = M2;
-                    oa = Operand{Ts + (n * Pp + ta) * ldt + i * M2, MT * ldt, 0};
-                    ob = Operand{Gs + (n * Qp + tb) * ldg, CT * ldg, 0};
+                    oa = Operand{Ts + (n * Pp + ta) * ldt + i * M2, MT * ldt, 4 * MT * ldt};
+                    ob = Operand{Gs + (n * Qp + 4 * tb) * ldg, ldg, 4 * CT * ldg};
                 }
                 const int slot = n;
                 for (; n < R; n += step) {
-                    mm8<true, true>(acc, oa, ob, K);
+                    mm8<true, true, false>(acc, oa, ob, K);
                     oa.p += step * Pp * ldt;
                     ob.p += step * Qp * ldg;
                 }
@@ -516,19 +519,21 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
                     for (int u = 0; u < 8; ++u) {
                         const int row = ta + u * MR, rn = row / Pp, a = row - rn * Pp;
                         if (rn >= R || a >= P || n0 + rn >= hi) continue;
-                        float *d = dX + ((n0 + rn) * P + a) * M1;
-#pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            if (tb + v * JT < M1) d[tb + v * JT] = acc[u][v];
+                        float *d = dX + ((n0 + rn) * P + a) * M1 + 4 * tb;
+                        *reinterpret_cast<float4 *>(d) =
+                            make_float4(acc[u][0], acc[u][1], acc[u][2], acc[u][3]);
+                        if (tb + JT < jq)
+                            *reinterpret_cast<float4 *>(d + 4 * JT) =
+                                make_float4(acc[u][4], acc[u][5], acc[u][6], acc[u][7]);
                     }
                 } else {
-                    float *d = Ss + slot * (n_dc + n_db) + i * P * Q;
+                    float *d = Ss + slot * n_slot + n_db + (i * P + ta) * Qp + 4 * tb;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-#pragma unroll
-                        for (int v = 0; v < 8; ++v)
-                            if (ta + u * MT < P && tb + v * CT < Q)
-                                d[(ta + u * MT) * Q + tb + v * CT] += acc[u][v];
+                    for (int u = 0; u < 8; ++u) {
+                        if (ta + u * MT >= P) break;
+                        add4(d + u * MT * Qp, &acc[u][0], first);
+                        if (4 * (tb + CT) < Qp) add4(d + u * MT * Qp + 4 * CT, &acc[u][4], first);
+                    }
                 }
             } else {
                 int e = t - n_x - n_c;
@@ -539,34 +544,35 @@ glu_f32_backward_kernel(const float *__restrict__ x, const float *__restrict__ S
                 const int i = e % r, slot = e / r;
                 if (slot >= pl.slots) continue;
                 for (int n = slot; n < R; n += pl.slots)
-                    mm8<false, false>(acc, Operand{Xs + n * Pp * ldx + 4 * tj, ldx, 4 * JT},
-                                      Operand{Us + n * Pp * ldt + i * M2 + 4 * tk, ldt, 4 * NT}, Pp);
-                float *d = Ss + slot * (n_dc + n_db) + n_dc + (size_t)i * M1 * M2;
+                    mm8<false, false, false>(
+                        acc, Operand{Xs + n * Pp * ldx + 4 * tj, ldx, 4 * JT},
+                        Operand{Us + n * Pp * ldt + i * M2 + 4 * tk, ldt, 4 * NT}, Pp);
+                float *d = Ss + slot * n_slot + (i * M1 + 4 * tj) * M2 + 4 * tk;
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    const int j = 4 * (tj + (u >> 2) * JT) + (u & 3);
-                    if (j >= M1) break;
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        if (tk + (v >> 2) * NT < nq)
-                            d[j * M2 + 4 * (tk + (v >> 2) * NT) + (v & 3)] += acc[u][v];
+                    if (tj + (u >> 2) * JT >= jq) break;
+                    float *du = d + (4 * (u >> 2) * JT + (u & 3)) * M2;
+                    add4(du, &acc[u][0], first);
+                    if (tk + NT < nq) add4(du + 4 * NT, &acc[u][4], first);
                 }
             }
         }
-        for (int e = threadIdx.x; e < Q * M2; e += kThreads) {
+        for (int e = threadIdx.x; e < Q * M2; e += kBackThreads) {
             const int c = e / M2, k = e - c * M2;
             float v = 0.f;
             for (int n = 0; n < R; ++n) v += Gs[(n * Qp + c) * ldg + k];
-            Ds[e] += v;
+            Ds[e] = first ? v : Ds[e] + v;
         }
         __syncthreads();
     }
-    for (int e = threadIdx.x; e < n_dc + n_db; e += kThreads) {
+    for (int e = threadIdx.x; e < n_slot; e += kBackThreads) {
         float v = 0.f;
-        for (int k = 0; k < pl.slots; ++k) v += Ss[k * (n_dc + n_db) + e];
-        out[e] = v;
+        for (int k = 0; k < pl.slots; ++k) v += Ss[k * n_slot + e];
+        const int row = (e - n_db) / Qp, c = e - n_db - row * Qp;
+        if (e < n_db) out[n_dc + e] = v;
+        else if (c < Q) out[row * Q + c] = v;
     }
-    for (int e = threadIdx.x; e < Q * M2; e += kThreads) out[n_dc + n_db + e] = Ds[e];
+    for (int e = threadIdx.x; e < Q * M2; e += kBackThreads) out[n_dc + n_db + e] = Ds[e];
 }
 
 // Ranges for one CTA per SM; the largest tile that fits shared memory, then as many slots.  At
@@ -586,7 +592,7 @@ bool backward_plan(BPlan *b, const Shape &s, int max_parts) {
         rk * s.m1 > 16384)
         return false;
     p.ldt = odd4((int)rk);
-    const int sums = (int)((int64_t)s.r * s.p * s.q + rk * s.m1);
+    const int sums = (int)((int64_t)s.r * s.p * p.Qp + rk * s.m1);
     // the last rows of a tensor are read up to seven rows further
     const int ld = p.ldt > p.ldc ? p.ldt : p.ldc, ld2 = p.ldx > p.ldg ? p.ldx : p.ldg;
     const int tail = 8 * (ld > ld2 ? ld : ld2);
@@ -603,7 +609,7 @@ bool backward_plan(BPlan *b, const Shape &s, int max_parts) {
         p.offS = p.offT + R * p.Pp * p.ldt;
         for (int slots = R; slots >= 1; --slots) {
             p.slots = slots;
-            p.offD = p.offS + up4i(slots * sums);
+            p.offD = p.offS + slots * sums;
             const int64_t words = p.offD + s.d_out() + tail;
             if (words * 4 > kMaxSmem) continue;
             p.smem = (int)words * 4;
@@ -656,10 +662,10 @@ cudaError_t f32_backward_pair(const void *x, const void *S, const void *A, const
                               const void *G0, const void *G1, void *dX0, void *dX1, float *ws,
                               int max_parts, int *parts, const Shape &s, cudaStream_t st) {
     BPlan p;
-    // the compiled shape has kernels of its own, faster where rows are many: 1024 rows 208 us here
-    // for the whole backward call and 211 there, 2368 rows 400 and 357, 20000 rows 2922 and 2278
+    // the compiled shape has kernels of its own, faster where rows are many: 2000 rows 335 us here
+    // for the whole backward call and 351 there, 2368 rows 384 and 355, 20000 rows 2778 and 2281
     const bool own = s.p == 32 && s.q == 32 && s.m1 == 32 && s.m2 == 32 && s.r == 4 &&
-                     s.N >= 10 * kRowParts;
+                     s.N >= kCompiledRows;
     if (own || !backward_plan(&p, s, max_parts)) {
         *parts = max_parts;
         return simt_backward_pair(x, S, A, B, G0, G1, dX0, dX1, ws, max_parts, s, st);
@@ -670,7 +676,7 @@ cudaError_t f32_backward_pair(const void *x, const void *S, const void *A, const
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
     if (e != cudaSuccess) return e;
     launch_step() = "backward launch";
-    glu_f32_backward_kernel<<<dim3((unsigned)p.parts, 2), kThreads, p.smem, st>>>(
+    glu_f32_backward_kernel<<<dim3((unsigned)p.parts, 2), kBackThreads, p.smem, st>>>(
         (const float *)x, (const float *)S, (const float *)A, (const float *)B, (const float *)G0,
         (const float *)G1, (float *)dX0, (float *)dX1, ws, partial_stride(s), s, p);
     return cudaGetLastError();

@@ -755,8 +755,8 @@ static double mma_cycles(int n) { return n > 208 ? n * 0.5 : 70 + n * 0.13; }
 
 // Chooses MP, the c slices and the ring by an estimate of the kernel's time: per chunk the
 // larger of its shared-memory cycles (128 B each) and its MMA cycles and about 80 of hand-over,
-// per tile at least epilogue 2's time, per CTA the packing of the factors.  More slices mean less packing per CTA and room for the factors, and more repeats of
-// stage 1 and of the reads of x.
+// per tile at least epilogue 2's time, per CTA the packing of the factors.  More slices mean less
+// packing per CTA and room for the factors, and more repeats of stage 1 and of the reads of x.
 static bool find_plan(Plan *best, const Shape &s, Mode mode, int sms) {
     double best_cost = 0;
     bool found = false;

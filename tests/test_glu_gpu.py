@@ -99,8 +99,11 @@ def test_f32(case):
 
 
 # several passes over the ranks, the last one shorter; several tiles per CTA in each form; a last
-# slice of k that is narrower; more columns c than one kernel takes
-F32_TILES = [(32, 32, 32, 32, 9, 300), (64, 64, 32, 32, 6, 2000), (8, 8, 12, 20, 3, 6000),
+# slice of k that is narrower; more columns c than one kernel takes; a backward in tiles of one and
+# of several slots, the last tile shorter, and in one that does not fit
+F32_TILES = [(30, 30, 32, 32, 4, 300), (5, 7, 4, 12, 1, 1000), (4, 36, 20, 8, 2, 149),
+             (48, 48, 24, 24, 1, 2000), (32, 32, 32, 32, 9, 300),
+             (64, 64, 32, 32, 6, 2000), (8, 8, 12, 20, 3, 6000),
              (40, 33, 28, 44, 5, 1200), (3, 70, 8, 100, 2, 33), (2, 2100, 4, 4, 1, 5)]
 
 
