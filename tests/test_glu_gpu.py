@@ -228,6 +228,41 @@ def test_stream_graph_and_repeat():
         assert torch.equal(g[k], fresh[k]), k
 
 
+@pytest.mark.parametrize("shape", [(30, 22, 12, 20, 2), (32, 32, 32, 32, 9)],
+                         ids=["one_pass", "several_passes"])
+def test_f32_nan_row_graph_and_last_row(shape):
+    N, (p, q, m1, m2, r) = 213, shape
+    d = make(N, *shape, dtype="f32", seed=3)
+    clean = run(d, "silu", "f32")
+    bad = {k: v.clone() for k, v in d.items()}
+    bad["x"][5, 3], bad["dH"][9, 7] = float("nan"), float("inf")
+    got = run(bad, "silu", "f32")
+    rows = torch.arange(N, device=DEV) != 5
+    assert torch.equal(got["h"][rows], clean["h"][rows]) and bool(got["h"][5].isnan().any())
+    rows &= torch.arange(N, device=DEV) != 9
+    assert torch.equal(got["dX"][rows], clean["dX"][rows])
+
+    fac = (d["x"], d["S"], d["A"], d["B"])
+    h = torch.full((N + 7, q * m2), 7.0, device=DEV)
+    grads = {"dX": torch.full((N + 7, p * m1), 7.0, device=DEV)[:N]}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        native.glu_forward(*fac, d["bias"], dtype="f32", out=h[:N])
+        g = native.glu_backward(*fac, d["dH"], d["bias"], dtype="f32", grads=grads)
+    other = make(N, *shape, dtype="f32", seed=4)
+    for k in d:
+        d[k].copy_(other[k])
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    fresh = run(d, "silu", "f32")
+    assert torch.equal(h[:N], fresh["h"]) and bool((h[N:] == 7).all())
+    for k in g:
+        assert torch.equal(g[k], fresh[k]), k
+    behind = torch.as_strided(grads["dX"], (7, p * m1), (p * m1, 1), N * p * m1)
+    assert bool((behind == 7).all())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_module_and_autograd(dtype):
     torch.manual_seed(0)
