@@ -461,7 +461,7 @@ def glu_forward(x, S, A, B, bias=None, activation="silu", dtype="bf16", out=None
     shape = (sizes[0], sizes[2] * sizes[4])
     with _on_device(dev, stream):
         if out is None:
-            out = torch.empty(shape, dtype=t, device=dev)
+            out = x.new_empty(shape)
         else:
             _need(out, "h", t, shape, dev)
         keep, ws, ws_bytes = _glu_workspace(sizes, dtype, False, workspace, dev)
@@ -486,7 +486,7 @@ def glu_backward(x, S, A, B, dH, bias=None, activation="silu", dtype="bf16", nee
             if not need:
                 g[k] = None
             elif g.get(k) is None:
-                g[k] = torch.empty(shp, dtype=t, device=dev)
+                g[k] = x.new_empty(shp)
             else:
                 _need(g[k], k, t, shp, dev)
         keep, ws, ws_bytes = _glu_workspace(sizes, dtype, True, workspace, dev)
@@ -540,7 +540,7 @@ def _distill_args(logits, values, indices, labels, weights, label_weight):
 def _dlogits(logits, out):
     N, V = logits.shape
     if out is None:
-        return torch.empty(N, V, dtype=logits.dtype, device=logits.device), V
+        return logits.new_empty((N, V)), V
     ld = _rows(out, "dlogits", logits.dtype, N, V)
     if out.device != logits.device:
         raise ValueError(f"dlogits is on {out.device}, not on {logits.device}")
@@ -553,8 +553,8 @@ def distill_forward(logits, values, indices, labels=None, weights=None, temperat
     N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
                                               label_weight)
     with _on_device(dev, stream):
-        loss = torch.empty(N, dtype=torch.float32, device=dev)
-        lse = torch.empty(N, 2, dtype=torch.float32, device=dev)
+        loss = values.new_empty(N)
+        lse = values.new_empty((N, 2))
         _check(load().kron_distill_forward(*head, loss.data_ptr(), lse.data_ptr(), N, V, K,
                                            temperature, label_weight, dtype,
                                            _raw_stream(stream, dev)))
@@ -585,7 +585,7 @@ def distill_step(logits, values, indices, labels=None, weights=None, temperature
     N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
                                               label_weight)
     with _on_device(dev, stream):
-        loss = torch.empty(N, dtype=torch.float32, device=dev)
+        loss = values.new_empty(N)
         out, ld_out = _dlogits(logits, out)
         _check(load().kron_distill_step(*head, loss.data_ptr(), out.data_ptr(), ld_out, N, V, K,
                                         temperature, label_weight, dtype,
