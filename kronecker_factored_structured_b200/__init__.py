@@ -208,7 +208,8 @@ class KronGatedFFN(torch.nn.Module):
 
 
 class DistillFunction(torch.autograd.Function):
-    """Autograd wrapper of the distillation loss: a loss per row, the gradient in the logits."""
+    """Autograd wrapper of the distillation loss: a loss per row, the gradients in the logits and,
+    where they need one, in the rows' weights."""
 
     @staticmethod
     def forward(ctx, logits, values, indices, labels, weights, temperature, label_weight):
@@ -222,9 +223,16 @@ class DistillFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dloss):
         logits, values, indices, labels, weights, lse = ctx.saved_tensors
-        d = native.distill_backward(logits, values, indices, lse, dloss.contiguous(), labels,
-                                    weights, ctx.temperature, ctx.label_weight)
-        return d, None, None, None, None, None, None
+        dloss = dloss.contiguous()
+        d = dw = None
+        if ctx.needs_input_grad[0]:
+            d = native.distill_backward(logits, values, indices, lse, dloss, labels, weights,
+                                        ctx.temperature, ctx.label_weight)
+        if ctx.needs_input_grad[4]:
+            # the row's loss without its weight, which the weighted one does not give at zero
+            dw = dloss * native.distill_forward(logits, values, indices, labels, None,
+                                                ctx.temperature, ctx.label_weight)["loss"]
+        return d, None, None, None, dw, None, None
 
 
 def distill_loss(logits, values, indices, labels=None, weights=None, temperature=1.0,
@@ -235,8 +243,9 @@ def distill_loss(logits, values, indices, labels=None, weights=None, temperature
     ``values`` (float32) and ``indices`` hold the teacher's logits of each row and their
     columns, an index outside the vocabulary being no entry; shapes are (..., V), (..., K) and
     (...).  ``weights`` multiplies the rows.  reduction: "none" (the rows' losses), "sum", or
-    "mean" (the sum over the sum of ``weights``, or over the rows without them).  The teacher
-    gets no gradient.
+    "mean" (the sum over the sum of ``weights``, or over the rows without them).  ``logits`` and
+    ``weights`` are differentiable (the backward forms the rows' losses again for the weights);
+    the teacher gets no gradient.
     """
     if reduction not in ("none", "sum", "mean"):
         raise ValueError(f"reduction must be 'none', 'sum' or 'mean', got {reduction!r}")

@@ -323,3 +323,36 @@ def test_stream_graph_and_repeat():
     fresh = native.distill_step(*args, **kw)
     torch.cuda.synchronize()
     assert torch.equal(c["loss"], fresh["loss"]) and torch.equal(c["dlogits"], fresh["dlogits"])
+
+
+@pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
+def test_gradient_of_the_weights(reduction):
+    """The rows' weights are differentiable: dloss times the loss of the row, and for "mean" the
+    denominator's part; a row of weight zero has one too."""
+    d = make(8, 777, 9, torch.float32, seed=16, holes=False)
+    d["weights"][3] = 0.0
+    tau, lam = 2.0, 0.3
+    rows, _, _ = reference(dict(d, weights=None), tau, lam)
+    w = d["weights"].double().cpu()
+    up = torch.randn(8, generator=torch.Generator().manual_seed(2))
+    leaf = d["weights"].clone().requires_grad_(True)
+    z = d["logits"].clone().requires_grad_(True)
+    loss = kfs.distill_loss(z, d["values"], d["indices"], d["labels"], leaf, temperature=tau,
+                            label_weight=lam, reduction=reduction)
+    if reduction == "none":
+        loss = (loss * up.to(DEV)).sum()
+    g, gz = torch.autograd.grad(loss, (leaf, z))
+    W = w.sum()
+    want = {"none": up.double() * rows, "sum": rows,
+            "mean": rows / W - (w * rows).sum() / W ** 2}[reduction]
+    # a row's loss as in check_loss; "mean" takes a sum over eight rows besides
+    x = d["logits"].double()
+    span = float((x.max() - x.min()) / tau + 20)
+    row_tol = EPS * ((1 - lam) * tau ** 2 * (2 + span) + lam * (2 + span * tau))
+    c = {"none": float(up.abs().max()), "sum": 1.0, "mean": 2 / float(W)}[reduction]
+    assert g.shape == leaf.shape and g.dtype == torch.float32
+    assert float((g.double().cpu() - want).abs().max()) <= c * (row_tol + 16 * 2.0 ** -24 *
+                                                                float(rows.abs().max()))
+    _, grad, size = reference(d, tau, lam, up if reduction == "none" else None)
+    c = 1 / W if reduction == "mean" else 1.0
+    check_grad(gz, c * grad, 2 * c * size, torch.float32)
