@@ -317,9 +317,13 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
     if constexpr (GRAD) {
         const float soft = hard_only || !any ? 0.f : coef * (1.f - g.lam) * g.tau;
         const float hard = g.lam != 0.f && label >= 0 ? coef * g.lam : 0.f;
+        __syncwarp();           // the row's gathers and entries are complete
+        if (soft == 0.f && hard == 0.f) {   // no term: zero, whatever the logits hold
+            for (int v = lane; v < V; v += 32) Vc::put(out + v, 0.f);
+            return;
+        }
         const Dense<E> dense(soft, hard, lse_t, lse_1, a);
         const float share = soft == 0.f ? 0.f : soft * its;
-        __syncwarp();           // the row's gathers and entries are complete
         for (int v = lane; v < V; v += 32) Vc::put(out + v, dense.one(Vc::get(x + v)));
         __syncwarp();
         bool listed = false;
@@ -527,6 +531,11 @@ distill_kernel(const Args g) {
     const float soft = hard_only || !any ? 0.f : coef * (1.f - g.lam) * g.tau;
     const float hard = g.lam != 0.f && label >= 0 ? coef * g.lam : 0.f;
     const Dense<E> dense(soft, hard, lse_t, lse_1, a);
+    if (soft == 0.f && hard == 0.f) {   // no term: zero, whatever the logits hold
+        __syncthreads();                // in place, every thread has read them
+        for (int v = tid; v < V; v += kThreads) Vc::put(out + v, 0.f);
+        return;
+    }
     // every gather of the row is done before it may be overwritten
     const bool dup = __syncthreads_or(twice), has_label = __syncthreads_or(listed);
     auto grad_vec = [&](const uint4 &u, int v) {

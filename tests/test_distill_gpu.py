@@ -356,3 +356,32 @@ def test_gradient_of_the_weights(reduction):
     _, grad, size = reference(d, tau, lam, up if reduction == "none" else None)
     c = 1 / W if reduction == "mean" else 1.0
     check_grad(gz, c * grad, 2 * c * size, torch.float32)
+
+
+@pytest.mark.parametrize("V", [999, 1999])
+@pytest.mark.parametrize("lam", [0.0, 0.4, 1.0])
+def test_rows_without_any_term(lam, V):
+    """No entries, and no label where the labels count: the row's loss is the constant zero, and
+    its gradient is zero whatever its logits hold."""
+    for dtype in (torch.float32, torch.bfloat16):
+        d = make(6, V, 8, dtype, seed=17, holes=False)
+        x = d["logits"]
+        x[0, 5], x[1, 7], x[2] = float("nan"), float("inf"), float("-inf")
+        x[4, 9] = float("nan")
+        d["labels"][:4] = -100
+        d["indices"][:3] = -1
+        d["values"][3] = float("-inf")               # entries without weight are none
+        if lam == 1.0:
+            d["indices"][:4] = d["indices"][5]       # entries do not count
+            d["values"][:4] = d["values"][5]
+        d["weights"][0] = 3.0
+        kw = dict(labels=d["labels"], weights=d["weights"], temperature=2.0, label_weight=lam)
+        args = (x, d["values"], d["indices"])
+        f = native.distill_forward(*args, **kw)
+        s = native.distill_step(*args, **kw)
+        b = native.distill_backward(*args, f["lse"], **kw)
+        for loss, grad in ((s["loss"], s["dlogits"]), (f["loss"], b)):
+            assert not loss[:4].any() and not grad[:4].any()
+            # a row that has a term still shows its NaN; the one behind it is as ever
+            assert bool(loss[4].isnan()) and bool(grad[4].isnan().any())
+            assert bool(loss[5].isfinite()) and bool(grad[5].isfinite().all())
