@@ -320,8 +320,8 @@ KRON_API kron_status_t kron_glu_backward(const void *x, const void *S, const voi
  *   labels  [N] int64; a label outside [0, V) (such as -100) is none: the row's second term
  *           is zero.  May be NULL when lam = label_weight is 0.
  *   weights [N] float32, NULL = ones.  A row of weight 0 gives loss 0 and gradient 0 whatever
- *           its logits hold, and so does one without any term (no entries or lam = 1, and no
- *           label or lam = 0).
+ *           its logits and dloss hold, and so does one without any term (no entries or lam = 1,
+ *           and no label or lam = 0).
  *   loss    [N] float32, not reduced
  *   lse     [N][2] float32: the log-sum-exp of the row at the temperature and at one, which
  *           kron_distill_backward takes (one that the gradient does not need repeats the

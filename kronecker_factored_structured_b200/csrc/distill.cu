@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
     const T *x = static_cast<const T *>(g.logits) + row * g.ld;
     T *out = GRAD ? static_cast<T *>(g.dlogits) + row * g.ld_out : nullptr;
     const float w = g.weights ? g.weights[row] : 1.f;
-    const float coef = GRAD ? (g.dloss ? w * g.dloss[row] : w) : w;
+    // weight 0 wins over an infinite or NaN dloss
+    const float coef = GRAD && g.dloss && w != 0.f ? w * g.dloss[row] : w;
     if (coef == 0.f) {
         if (STATS && lane == 0) {
             g.loss[row] = 0.f;
@@ -358,7 +359,8 @@ distill_kernel(const Args g) {
     const T *x = static_cast<const T *>(g.logits) + row * g.ld;
     T *out = GRAD ? static_cast<T *>(g.dlogits) + row * g.ld_out : nullptr;
     const float w = g.weights ? g.weights[row] : 1.f;
-    const float coef = GRAD ? (g.dloss ? w * g.dloss[row] : w) : w;
+    // weight 0 wins over an infinite or NaN dloss
+    const float coef = GRAD && g.dloss && w != 0.f ? w * g.dloss[row] : w;
     const int V = g.V, K = g.K;
 
     // 16-byte body of the row, aligned for the logits; the gradient's vector stores also

@@ -385,3 +385,17 @@ def test_rows_without_any_term(lam, V):
             # a row that has a term still shows its NaN; the one behind it is as ever
             assert bool(loss[4].isnan()) and bool(grad[4].isnan().any())
             assert bool(loss[5].isfinite()) and bool(grad[5].isfinite().all())
+
+
+@pytest.mark.parametrize("V", [300, 3000])
+def test_weight_zero_meets_an_infinite_upstream_gradient(V):
+    """All weights zero under "mean" divides by zero: the rows' gradients stay zero, also where
+    the gradient that comes in is infinite or NaN."""
+    d = make(4, V, 9, torch.float32, seed=18, holes=False)
+    d["weights"][1] = d["weights"][2] = 0.0
+    kw = dict(labels=d["labels"], weights=d["weights"], temperature=2.0, label_weight=0.3)
+    args = (d["logits"], d["values"], d["indices"])
+    lse = native.distill_forward(*args, **kw)["lse"]
+    up = torch.tensor([1.0, float("inf"), float("nan"), float("nan")], device=DEV)
+    g = native.distill_backward(*args, lse, up, **kw)
+    assert not g[1:3].any() and bool(g[0].isfinite().all()) and bool(g[3].isnan().any())
