@@ -112,10 +112,28 @@ __device__ __forceinline__ float act_f32(int act, float g, float *d) {
 }
 
 // Activation, and with GRAD its derivative, of two values, from hardware exponentials and
-// reciprocals (about 2^-21 of the value: far below the bfloat16 rounding of what is stored).
+// reciprocals: about 2^-21 of the value (gelu 2^-17) and, of the terms that a derivative is the sum
+// of, of each, far below the bfloat16 rounding of what is stored.  In the tails an argument of size
+// v is rounded, 2^-23 v of an exponential, and one that overflows gives 0.
 __device__ __forceinline__ f2 sigmoid2(f2 g) {
     // an exponential that overflows gives 0
     return rcp_2(add2(ex2_2(mul2(g, dup2(-1.4426950408889634f))), dup2(1.f)));
+}
+
+// (1 + erf(g / sqrt 2)) / 2, e = exp(-g^2 / 2): the lower tail as e times a polynomial in 1 / (1 +
+// 0.31 |g|), a minimax fit of degree 6 without constant term, 2^-17.6 of the tail for |g| <= 14, where
+// e vanishes; the upper one is 1 less that, and neither cancels.  (Scalar: in packed arithmetic gelu
+// took 48 us instead of 49 for 20000 x 1024, r = 4, but silu, in the same kernel, 45.7 instead of
+// 43.6.  erff: 55, and nothing left of the value below g = -5.)
+__device__ __forceinline__ float normal_cdf(float g, float e) {
+    const float t = rcp(fmaf(fabsf(g), 0.31f, 1.f));
+    float c = fmaf(t, -0.0739276037f, 0.1804459095f);
+    c = fmaf(t, c, 0.0157496296f);
+    c = fmaf(t, c, 0.1334271729f);
+    c = fmaf(t, c, 0.120441936f);
+    c = fmaf(t, c, 0.1238606423f);
+    c *= t * e;
+    return g < 0.f ? c : 1.f - c;
 }
 
 template <int ACT, bool GRAD>
@@ -126,18 +144,22 @@ __device__ __forceinline__ f2 act2(f2 g, f2 &d) {
         return f;
     } else if constexpr (ACT == KRON_ACT_SIGMOID) {
         const f2 s = sigmoid2(g);
-        if (GRAD) d = mul2(s, fma2(s, dup2(-1.f), dup2(1.f)));
+        if (GRAD) {
+            // 1 - s as exp(-g) s, which keeps its bits where s is next to 1; s is 0 where exp(-g)
+            // is infinite
+            float t0, t1;
+            unpack2(ex2_2(mul2(g, dup2(-1.4426950408889634f))), t0, t1);
+            d = mul2(s, mul2(s, pack2(fminf(t0, 3.4e38f), fminf(t1, 3.4e38f))));
+        }
         return s;
     } else if constexpr (ACT == KRON_ACT_GELU) {
-        float lo, hi;
+        float lo, hi, e0, e1;
         unpack2(g, lo, hi);
-        const f2 c = fma2(pack2(erff(lo * 0.70710678f), erff(hi * 0.70710678f)), dup2(0.5f),
-                          dup2(0.5f));
+        const f2 e = ex2_2(mul2(mul2(g, g), dup2(-0.72134752f)));     // exp(-g^2 / 2)
+        unpack2(e, e0, e1);
+        const f2 c = pack2(normal_cdf(lo, e0), normal_cdf(hi, e1));
         if (GRAD) {
             // g exp(-g^2 / 2) / sqrt(2 pi); nothing where the exponential vanishes
-            const f2 e = ex2_2(mul2(mul2(g, g), dup2(-0.72134752f)));
-            float e0, e1;
-            unpack2(e, e0, e1);
             const f2 gz = pack2(e0 == 0.f ? 0.f : lo, e1 == 0.f ? 0.f : hi);
             d = fma2(mul2(gz, e), dup2(0.39894228f), c);
         }

@@ -391,3 +391,49 @@ def test_given_workspace_and_outputs():
         native.glu_backward(*fac, sq["dH"], sq["bias"], grads={"dX": sq["x"]})
     with pytest.raises(native.KronError):
         native.glu_forward(*fac, sq["bias"], out=sq["x"])
+
+
+def _tails(g, name):
+    """act(g), act'(g) and the terms that act' is the sum of, in absolute value; in 64 bits, in
+    forms that do not cancel (1 + tanh(v) = 2 sigmoid(2 v), 1 + erf(v) = erfc(-v))."""
+    if name == "gelu":
+        c = torch.special.erfc(-g / math.sqrt(2)) / 2
+        slope = g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+        return g * c, c + slope, c + slope.abs(), 1 + g.abs()
+    v, dv = g, torch.ones_like(g)
+    if name == "gelu_tanh":
+        v = math.sqrt(8 / math.pi) * (g + 0.044715 * g ** 3)
+        dv = math.sqrt(8 / math.pi) * (1 + 0.134145 * g ** 2)
+    s, c = torch.sigmoid(v), torch.sigmoid(-v)
+    if name == "sigmoid":
+        return s, s * c, s * c, 1 + 0 * g
+    return g * s, s + g * dv * s * c, s + (g * dv).abs() * s * c, 1 + (g * dv).abs()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("name", ACTS)
+def test_tails_of_the_activations(name, dtype):
+    """x = 0, so the bias is the pre-activation: the activation and its derivative alone, to
+    their own size.  f32: 2^-20 for the functions, and exponents of up to 150 rounded once or
+    twice (2 * 150 * 2^-24 < 2^-15 of an exponential); bf16: 2^-8 besides, for the rounding of
+    what is stored.  An exponential of 2^126 or more may be infinite, so that what it divides is
+    zero: 2^-126 of the factors that it has."""
+    g = torch.arange(-96, 161, dtype=torch.float64).div(8)            # -12 to 20
+    d = make(1, 2, 33, 8, 8, 1, dtype=dtype)
+    bias = torch.ones(2, 264, dtype=torch.float64)
+    bias[0, : g.numel()] = g
+    g = bias[0]
+    d["x"].zero_()
+    d["dH"].fill_(1.0)
+    d["bias"] = bias.to(native.io_dtype(dtype)).to(DEV)
+    assert torch.equal(d["bias"].double().cpu(), bias)                # nothing is rounded
+    out = run(d, name, dtype)
+    f, df, terms, factor = _tails(g, name)
+    fn = 2.0 ** -15 + 2.0 ** -20
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    low = 2.0 ** -126 * factor
+    err = (out["h"][0].double().cpu() - f).abs()
+    assert bool((err <= (fn + half) * f.abs() + low).all()), g[err > (fn + half) * f.abs() + low]
+    # of one row: the column sum is dg itself
+    err, tol = (out["dbias"][0].double().cpu() - df).abs(), fn * terms + half * df.abs() + low
+    assert bool((err <= tol).all()), g[err > tol]
