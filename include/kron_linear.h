@@ -325,7 +325,8 @@ KRON_API kron_status_t kron_glu_backward(const void *x, const void *S, const voi
  *   loss    [N] float32, not reduced
  *   lse     [N][2] float32: the log-sum-exp of the row at the temperature and at one, which
  *           kron_distill_backward takes (one that the gradient does not need repeats the
- *           other); forward: may be NULL
+ *           other); forward: may be NULL.  The backward forms the sums of a row again
+ *           where one is above 1024 in size, whose rounding would be 1e-4 of a probability
  *   dloss   [N] float32, the gradient of `loss`, NULL = ones
  *   dlogits rows ld_out elements apart, of the logits' type; may be the logits themselves
  *           (the same pointer and stride), and does not overlap them otherwise

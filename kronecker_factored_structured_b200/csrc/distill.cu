@@ -6,11 +6,12 @@
 //   loss = w [ (1 - lam) tau^2 sum_j p_j (log p_j - log q_{i_j}) + lam (lse(x) - x_label) ]
 //   dx_v = w dl [ (1 - lam) tau (q_v - sum_{j: i_j = v} p_j) + lam (softmax(x)_v - [v = label]) ]
 //
-// One CTA of 256 threads per row, six per SM (more threads where there are few rows).  Pass 1 reads the row with a running maximum m per
-// thread and the sums of exp((x - m)/tau) and exp(x - m); pass 2 (gradient) reads it again, from
-// L2, and writes the dense part c_t q + c_1 softmax(x); the K + 1 columns that the teacher and
-// the label touch are then overwritten by the thread that owns the first entry of the column,
-// in fp32, from logits fetched before anything is written (so dlogits may be the logits).
+// One CTA of 256 threads per row, five or six per SM (more threads where there are few rows).  Pass
+// 1 reads the row with a running maximum m per thread and the sums of exp((x - m)/tau) and
+// exp(x - m); pass 2 (gradient) reads it again and writes the dense part c_t q + c_1 softmax(x); the
+// K + 1 columns that the teacher and the label touch are then overwritten by the thread that owns
+// the first entry of the column, in fp32, from logits fetched before anything is written (so dlogits
+// may be the logits).  Exponents are differences from a value next to the maximum, never from zero.
 // Bound: HBM moves the logits once in and once out (126 us for 4096 x 50257 bf16); per element
 // and pass one ex2 (two for a tau other than 1, 2 and 4), 92 us on the special-function units,
 // and with the packed FP32 instructions some 11 issue slots.  Measured 177 us (scalar FP32
@@ -163,6 +164,13 @@ template <int E> __device__ __forceinline__ Stat shuffle_xor(const Stat &st, int
     return t;
 }
 
+// What the columns that are written last need: what is subtracted from their logits first, the
+// coefficients of the teacher's and the label's share, the label's logit and the label.
+struct Last {
+    float at, share, hard, xlab;
+    int label;
+};
+
 // What a row needs of the teacher, in shared memory: columns (-1: no entry), probabilities,
 // student logits at the columns.
 struct RowSmem {
@@ -172,8 +180,7 @@ struct RowSmem {
     Stat warp[32];
     float red[32];
     float redm[32];
-    Stat row;
-    float tsum;
+    Last last;
 };
 
 // Sum over the CTA in a fixed order; every thread gets it.
@@ -198,22 +205,66 @@ __device__ __forceinline__ float block_max(float v, float *red) {
     return t;
 }
 
+// Where a row's probabilities are read off: q = exp((x - at)/tau) exp(t), softmax(x) =
+// exp(x - at) exp(one), with `at` next to the row's maximum: the exponents are small however far
+// from zero the logits are.
+struct Origin {
+    float at, t, one;
+};
+// From pass 1: the maximum and the logarithms of the two sums.
+__device__ __forceinline__ Origin origin_of(float m, float lsum_t, float lsum_1) {
+    return {m, -lsum_t, -lsum_1};
+}
+// From the log-sum-exps, in 64 bits: no error but theirs.  With one exponential only the one at its
+// temperature is known.
+template <int E> __device__ __forceinline__ Origin origin_of(const float *lse, float tau, bool hard) {
+    const float lse_t = hard ? lse[1] : lse[0], at = E == kOne ? (float)((double)lse_t * tau) : lse[1];
+    const float t = (float)((double)at / tau - lse_t);
+    return {at, t, E == kOne ? t : 0.f};
+}
+// Rounding a log-sum-exp moves every probability by 2^-24 of its size (its products with 1/tau by
+// half as much): beyond this size, 1e-4 of a probability, a gradient forms the sums again.
+constexpr float kLseMax = 1024.f;
+__device__ __forceinline__ bool lse_is_near(const float *lse) {
+    return fabsf(lse[0]) <= kLseMax && fabsf(lse[1]) <= kLseMax;
+}
+
+// The threads' statistics merged in a fixed order; every thread gets the row's.
+template <int E, int kThreads>
+__device__ __forceinline__ Stat block_stat(Stat st, float a, Stat *warp) {
+    for (int o = 16; o; o >>= 1) {
+        const Stat t = shuffle_xor<E>(st, o);
+        merge<E>(st, t, a);
+    }
+    if ((threadIdx.x & 31) == 0) warp[threadIdx.x >> 5] = st;
+    __syncthreads();
+    Stat r = warp[0];
+    for (int i = 1; i < kThreads / 32; ++i) merge<E>(r, warp[i], a);
+    return r;
+}
+
 // The dense part of a row's gradient, soft q + hard softmax(x), of one or two logits.
 template <int E> struct Dense {
     f2 a, b, ct, c1, b1;
-    // a: log2(e) / tau (or log2(e), where only the label's term is there)
-    __device__ __forceinline__ Dense(float soft, float hard, float lse_t, float lse_1, float scale) {
-        // exp(x - lse_1) from q: (q exp(lse_t - lse_1/tau))^tau, the factor in [1, V]; with its
-        // power in the coefficient
-        const float lift = E == kSquare ? ex2((lse_t - 0.5f * lse_1) * kLog2e)
-                                        : E == kFourth ? ex2((lse_t - 0.25f * lse_1) * kLog2e)
-                                                       : 1.f;
-        const float l2 = lift * lift;
+    // Whether (x - at) a is formed as one multiply-add x a + b whose rounded constant the
+    // coefficients make up for; else the caller subtracts `at` first (a fourth instruction in packed
+    // arithmetic, which took 197 us instead of 181 for 4096 x 50257 bf16, tau = 2, with the loss).
+    static __device__ __forceinline__ bool is_near(const Origin &o, float scale) {
+        return fabsf(o.at * scale) <= 0x1p24f && (E != kTwo || fabsf(o.at * kLog2e) <= 0x1p24f);
+    }
+    // scale: log2(e) / tau (or log2(e), where only the label's term is there)
+    __device__ __forceinline__ Dense(float soft, float hard, const Origin &o, float scale) {
+        const bool near = is_near(o, scale);
+        const float bt = near ? -o.at * scale : 0.f, bo = near ? -o.at * kLog2e : 0.f;
+        // what is left of at a + b, at most 1
+        const float rt = near ? fmaf(o.at, scale, bt) : 0.f, ro = near ? fmaf(o.at, kLog2e, bo) : 0.f;
+        const float r1 = E == kSquare ? 2.f * rt : E == kFourth ? 4.f * rt : E == kTwo ? ro : rt;
+        const float ft = soft * ex2(fmaf(o.t, kLog2e, -rt)), f1 = hard * ex2(fmaf(o.one, kLog2e, -r1));
         a = dup2(scale);
-        b = dup2(-lse_t * kLog2e);
-        b1 = dup2(-lse_1 * kLog2e);
-        ct = dup2(E == kOne ? soft + hard : soft);
-        c1 = dup2(E == kSquare ? hard * l2 : E == kFourth ? hard * (l2 * l2) : hard);
+        b = dup2(bt);
+        b1 = dup2(bo);
+        ct = dup2(E == kOne ? ft + f1 : ft);
+        c1 = dup2(f1);
     }
     __device__ __forceinline__ f2 two(f2 v) const {
         const f2 e = ex2_2(fma2(v, a, b));
@@ -283,17 +334,22 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
     for (int o = 16; o; o >>= 1) ts += __shfl_xor_sync(0xffffffffu, ts, o);
     const bool any = ts != 0.f;
     const float its = any ? 1.f / ts : 0.f;
-    float lse_t, lse_1;
-    if constexpr (STATS) {
-        Stat st{-INFINITY, 0.f, 0.f};
+    Origin origin;
+    Stat st{-INFINITY, 0.f, 0.f};
+    float lsum = 0.f, lsum1 = 0.f;
+    if (STATS || !lse_is_near(g.lse_in + 2 * row)) {
         for (int v = lane; v < V; v += 32) add_one<E>(st, Vc::get(x + v), a);
         for (int o = 16; o; o >>= 1) {
             const Stat t = shuffle_xor<E>(st, o);
             merge<E>(st, t, a);
         }
-        const float lsum = logf(st.s);
-        lse_t = st.m * inv_tau + lsum;
-        lse_1 = E == kOne ? lse_t : st.m + logf(st.s1);
+        // (with one exponential and both terms, tau is 1 and the two agree)
+        lsum = logf(st.s), lsum1 = E == kOne ? lsum : logf(st.s1);
+        origin = origin_of(st.m, lsum, lsum1);
+    } else {
+        origin = origin_of<E>(g.lse_in + 2 * row, hard_only ? 1.f : g.tau, hard_only);
+    }
+    if constexpr (STATS) {
         const float llse = logf(ts);
         float kl = 0.f;
         if (!hard_only)
@@ -304,16 +360,13 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
         for (int o = 16; o; o >>= 1) kl += __shfl_xor_sync(0xffffffffu, kl, o);
         if (lane == 0) {
             float l = (1.f - g.lam) * g.tau * g.tau * kl;
-            if (g.lam != 0.f && label >= 0) l += g.lam * (lse_1 - xlab);
+            if (g.lam != 0.f && label >= 0) l += g.lam * (st.m - xlab + lsum1);
             g.loss[row] = w * l;
             if (g.lse) {
-                g.lse[2 * row] = lse_t;
-                g.lse[2 * row + 1] = lse_1;
+                g.lse[2 * row] = st.m * inv_tau + lsum;
+                g.lse[2 * row + 1] = E == kOne ? st.m * inv_tau + lsum : st.m + lsum1;
             }
         }
-    } else {
-        lse_t = hard_only ? g.lse_in[2 * row + 1] : g.lse_in[2 * row];
-        lse_1 = g.lse_in[2 * row + 1];
     }
     if constexpr (GRAD) {
         const float soft = hard_only || !any ? 0.f : coef * (1.f - g.lam) * g.tau;
@@ -323,9 +376,10 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
             for (int v = lane; v < V; v += 32) Vc::put(out + v, 0.f);
             return;
         }
-        const Dense<E> dense(soft, hard, lse_t, lse_1, a);
+        const Dense<E> dense(soft, hard, origin, a);
+        const float at = Dense<E>::is_near(origin, a) ? 0.f : origin.at;
         const float share = soft == 0.f ? 0.f : soft * its;
-        for (int v = lane; v < V; v += 32) Vc::put(out + v, dense.one(Vc::get(x + v)));
+        for (int v = lane; v < V; v += 32) Vc::put(out + v, dense.one(Vc::get(x + v) - at));
         __syncwarp();
         bool listed = false;
         for (int j = lane; j < K; j += 32) {
@@ -340,16 +394,34 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
                     p += prob[k];
                 }
             if (first)
-                Vc::put(out + c, dense.one(xs[j]) - (share == 0.f ? 0.f : share * p) -
+                Vc::put(out + c, dense.one(xs[j] - at) - (share == 0.f ? 0.f : share * p) -
                                      (c == label ? hard : 0.f));
         }
         listed = __any_sync(0xffffffffu, listed);
-        if (lane == 0 && label >= 0 && !listed) Vc::put(out + label, dense.one(xlab) - hard);
+        if (lane == 0 && label >= 0 && !listed) Vc::put(out + label, dense.one(xlab - at) - hard);
     }
 }
 
+// A row's sums formed again by a gradient, for log-sum-exps that are too far from zero.  A call: its
+// registers are not the gradient's.
+template <typename T, int E, int kThreads>
+__device__ __noinline__ Origin far_origin(const T *x, int V, float a, Stat *warp) {
+    Stat st{-INFINITY, 0.f, 0.f};
+    for (int v = threadIdx.x; v < V; v += kThreads) add_one<E>(st, Vec<T>::get(x + v), a);
+    const Stat r = block_stat<E, kThreads>(st, a, warp);
+    const float lsum = logf(r.s);
+    return origin_of(r.m, lsum, E == kOne ? lsum : logf(r.s1));
+}
+
+// Threads per SM for which registers are set aside.  Loss and gradient in one kernel take five CTAs of
+// 256 threads (48 registers) rather than six (40): 4096 x 50257 bf16 at tau = 1, 2 and 4 183, 188 and
+// 195 us and 192, 188 and 191; 1023 x 32000 38, 39 and 41 us and 42, 41 and 43.
+constexpr int threads_per_sm(bool stats, bool grad, int threads) {
+    return !stats ? 2048 : grad && threads == 256 ? 1280 : 1536;
+}
+
 template <typename T, int E, bool STATS, bool GRAD, int kThreads>
-__global__ void __launch_bounds__(kThreads, (STATS ? 1536 : 2048) / kThreads)
+__global__ void __launch_bounds__(kThreads, threads_per_sm(STATS, GRAD, kThreads) / kThreads)
 distill_kernel(const Args g) {
     __shared__ RowSmem sm;
     using Vc = Vec<T>;
@@ -435,7 +507,7 @@ distill_kernel(const Args g) {
     const float its = any ? 1.f / ts : 0.f;
 
     // ---- the student's log-sum-exp at both temperatures
-    float lse_t, lse_1;
+    Origin origin;
     if constexpr (STATS) {
         Stat st{-INFINITY, 0.f, 0.f};
         // sums of the thread's even and odd elements, relative to st.m
@@ -488,18 +560,10 @@ distill_kernel(const Args g) {
         if (tid < head) add_one<E>(st, Vc::get(x + tid), a);
         const int tail = head + nv * n + tid;
         if (tail < V) add_one<E>(st, Vc::get(x + tail), a);
-        for (int o = 16; o; o >>= 1) {
-            const Stat t = shuffle_xor<E>(st, o);
-            merge<E>(st, t, a);
-        }
-        if ((tid & 31) == 0) sm.warp[tid >> 5] = st;
-        __syncthreads();
-        Stat r = sm.warp[0];
-        for (int i = 1; i < kThreads / 32; ++i) merge<E>(r, sm.warp[i], a);
-        const float lsum = logf(r.s);
-        lse_t = r.m * inv_tau + lsum;
-        lse_1 = E == kOne ? lse_t : r.m + logf(r.s1);
+        const Stat r = block_stat<E, kThreads>(st, a, sm.warp);
         // (with one exponential and both terms, tau is 1 and the two agree)
+        const float lsum = logf(r.s), lsum1 = E == kOne ? lsum : logf(r.s1);
+        origin = origin_of(r.m, lsum, lsum1);
 
         // ---- the loss
         const float llse = logf(ts);
@@ -516,23 +580,27 @@ distill_kernel(const Args g) {
         kl = block_sum<kThreads>(kl, sm.red);
         if (tid == 0) {
             float l = (1.f - g.lam) * g.tau * g.tau * kl;
-            if (g.lam != 0.f && label >= 0) l += g.lam * (lse_1 - xlab);
+            if (g.lam != 0.f && label >= 0) l += g.lam * (r.m - xlab + lsum1);
             g.loss[row] = w * l;
             if (g.lse) {
-                g.lse[2 * row] = lse_t;
-                g.lse[2 * row + 1] = lse_1;
+                g.lse[2 * row] = r.m * inv_tau + lsum;
+                g.lse[2 * row + 1] = E == kOne ? r.m * inv_tau + lsum : r.m + lsum1;
             }
         }
+    } else if (lse_is_near(g.lse_in + 2 * row)) {
+        origin = origin_of<E>(g.lse_in + 2 * row, hard_only ? 1.f : g.tau, hard_only);
     } else {
-        lse_t = hard_only ? g.lse_in[2 * row + 1] : g.lse_in[2 * row];
-        lse_1 = g.lse_in[2 * row + 1];
+        origin = far_origin<T, E, kThreads>(x, V, a, sm.warp);
     }
     if constexpr (!GRAD) return;
 
     // ---- the gradient: c_t q + c_1 softmax(x), less the teacher's and the label's share
     const float soft = hard_only || !any ? 0.f : coef * (1.f - g.lam) * g.tau;
     const float hard = g.lam != 0.f && label >= 0 ? coef * g.lam : 0.f;
-    const Dense<E> dense(soft, hard, lse_t, lse_1, a);
+    const Dense<E> dense(soft, hard, origin, a);
+    const bool near = Dense<E>::is_near(origin, a);
+    Last last{near ? 0.f : origin.at, soft == 0.f ? 0.f : soft * its, hard, xlab, label};
+    if (STATS && tid == 0) sm.last = last;
     if (soft == 0.f && hard == 0.f) {   // no term: zero, whatever the logits hold
         __syncthreads();                // in place, every thread has read them
         for (int v = tid; v < V; v += kThreads) Vc::put(out + v, 0.f);
@@ -558,20 +626,25 @@ distill_kernel(const Args g) {
             }
         }
     };
-    int v = tid;
-    for (; v + 3 * kThreads < nv; v += 4 * kThreads) {
-        uint4 u[4];
+    if (near) {
+        int v = tid;
+        for (; v + 3 * kThreads < nv; v += 4 * kThreads) {
+            uint4 u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = __ldcs(xv + v + i * kThreads);
+            for (int i = 0; i < 4; ++i) u[i] = __ldcs(xv + v + i * kThreads);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) grad_vec(u[i], v + i * kThreads);
+            for (int i = 0; i < 4; ++i) grad_vec(u[i], v + i * kThreads);
+        }
+        for (; v < nv; v += kThreads) grad_vec(__ldcs(xv + v), v);
+        if (tid < head) Vc::put(out + tid, dense.one(Vc::get(x + tid)));
+        const int tail = head + nv * n + tid;
+        if (tail < V) Vc::put(out + tail, dense.one(Vc::get(x + tail)));
+    } else {
+        for (int v = tid; v < V; v += kThreads) Vc::put(out + v, dense.one(Vc::get(x + v) - last.at));
     }
-    for (; v < nv; v += kThreads) grad_vec(__ldcs(xv + v), v);
-    if (tid < head) Vc::put(out + tid, dense.one(Vc::get(x + tid)));
-    const int tail = head + nv * n + tid;
-    if (tail < V) Vc::put(out + tail, dense.one(Vc::get(x + tail)));
     __syncthreads();
-    const float share = soft == 0.f ? 0.f : soft * its;
+    // with the loss in the same kernel there are no registers to keep these over the dense pass
+    if constexpr (STATS) last = sm.last;
     for (int j = tid; j < K; j += kThreads) {
         const int c = sm.col[j];
         if (c < 0) continue;
@@ -586,10 +659,12 @@ distill_kernel(const Args g) {
                 }
         }
         if (first)
-            Vc::put(out + c, dense.one(sm.x[j]) - (share == 0.f ? 0.f : share * p) -
-                                 (c == label ? hard : 0.f));
+            Vc::put(out + c, dense.one(sm.x[j] - last.at) -
+                                 (last.share == 0.f ? 0.f : last.share * p) -
+                                 (c == last.label ? last.hard : 0.f));
     }
-    if (tid == 0 && label >= 0 && !has_label) Vc::put(out + label, dense.one(xlab) - hard);
+    if (tid == 0 && last.label >= 0 && !has_label)
+        Vc::put(out + last.label, dense.one(last.xlab - last.at) - last.hard);
 }
 
 kron_status_t bad(kron_status_t st, const char *fmt, double a = 0, double b = 0) {

@@ -399,3 +399,71 @@ def test_weight_zero_meets_an_infinite_upstream_gradient(V):
     up = torch.tensor([1.0, float("inf"), float("nan"), float("nan")], device=DEV)
     g = native.distill_backward(*args, lse, up, **kw)
     assert not g[1:3].any() and bool(g[0].isfinite().all()) and bool(g[3].isnan().any())
+
+
+@pytest.mark.parametrize("V", [1000, 5000])
+@pytest.mark.parametrize("tau,lam", [(1.0, 0.0), (1.0, 0.4), (2.0, 0.5), (4.0, 0.3), (1.5, 0.5),
+                                     (3.0, 0.0), (1.0, 1.0)])
+def test_logits_far_from_zero(tau, lam, V):
+    """A common offset of the logits drops out of the softmax: loss and gradient are as exact with
+    it as without.  The backward takes log-sum-exps of up to 1024 as they are, rounded to 2^-24 of
+    their size, and their products with 1/tau by half as much."""
+    for offset in (300.0, 1e4, -3e5):
+        d = make(7, V, 16, torch.float32, seed=19, holes=False)
+        d["logits"] += offset
+        ref, grad, size = reference(d, tau, lam)
+        kw = dict(labels=d["labels"], weights=d["weights"], temperature=tau, label_weight=lam)
+        args = (d["logits"], d["values"], d["indices"])
+        s = native.distill_step(*args, **kw)
+        f = native.distill_forward(*args, **kw)
+        # a log-probability is a difference of at most 30 (a rounding or two of it, 4e-6) and a
+        # logarithm that is off by 3e-5 at most; so is the loss, which averages them
+        tol = d["weights"].double().cpu() * ((1 - lam) * tau ** 2 + lam) * 6e-5
+        for got in (s["loss"], f["loss"]):
+            assert bool(((got.double().cpu() - ref).abs() <= tol).all())
+        check_grad(s["dlogits"], grad, size, torch.float32)
+        got = native.distill_backward(*args, f["lse"], **kw)
+        check_grad(got, grad, size * (1 + 1.5 * 1024 * 2.0 ** -24 / EPS), torch.float32)
+
+
+@pytest.mark.parametrize("V", [300, 3001])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_rows_of_extreme_logits(dtype, V):
+    """Rows that a mask has filled with the type's lowest value, or with one far from zero, are
+    uniform; beside one logit above the rest they are a point."""
+    for tau, lam in ((1.0, 0.0), (1.0, 0.5), (2.0, 0.5), (4.0, 0.5), (1.5, 0.5), (3.0, 0.0), (0.5, 1.0)):
+        d = make(6, V, 8, dtype, seed=21, holes=False)
+        x = d["logits"]
+        x[0], x[1], x[2], x[3] = torch.finfo(dtype).min, -1e9, torch.finfo(dtype).max, 3e10
+        x[4] = torch.finfo(dtype).min
+        x[4, 7] = 1.0
+        d["indices"][4], d["labels"][4] = 7, 7       # else its loss is infinite
+        ref, grad, size = reference(d, tau, lam)
+        kw = dict(labels=d["labels"], weights=d["weights"], temperature=tau, label_weight=lam)
+        args = (x, d["values"], d["indices"])
+        s = native.distill_step(*args, **kw)
+        f = native.distill_forward(*args, **kw)
+        b = native.distill_backward(*args, f["lse"], **kw)
+        tol = d["weights"].double().cpu() * ((1 - lam) * tau ** 2 + lam) * 6e-5
+        assert bool(((s["loss"].double().cpu() - ref).abs() <= tol).all())
+        assert torch.equal(s["loss"], f["loss"])
+        # entries of row 4 lie on one column, whose share is their sum
+        check_grad(s["dlogits"], grad, 2 * size, dtype)
+        check_grad(b, grad, 2 * size, dtype)
+
+
+@pytest.mark.parametrize("tau", [0.05, 100.0, 1000.0])
+def test_extreme_temperatures(tau):
+    for V in (900, 4001):
+        d = make(6, V, 8, torch.float32, seed=22, holes=False)
+        ref, grad, size = reference(d, tau, 0.3)
+        kw = dict(labels=d["labels"], weights=d["weights"], temperature=tau, label_weight=0.3)
+        args = (d["logits"], d["values"], d["indices"])
+        s = native.distill_step(*args, **kw)
+        # exponents of up to (range of 40) / tau carry two roundings of their size; the rest as in
+        # the file's head
+        eps = EPS + 2 * max(1.0, 40 / tau) * 2.0 ** -24
+        check_grad(s["dlogits"], grad, size * eps / EPS, torch.float32)
+        lse = native.distill_forward(*args, **kw)["lse"]
+        eps += 1.5 * 1024 * 2.0 ** -24
+        check_grad(native.distill_backward(*args, lse, **kw), grad, size * eps / EPS, torch.float32)
