@@ -24,6 +24,8 @@ namespace glu {
 namespace {
 
 constexpr int kThreads = 256, kBackThreads = 384;
+// Also every kernel's limit, whatever the size of a call's tiles: the limit is shared by the host
+// threads that call it.
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kHalf = kThreads / 2;    // stage-2 items
 
@@ -649,7 +651,7 @@ cudaError_t f32_pre(const void *x, const void *S, const void *A, const void *B, 
     auto *f = p.G < s.r ? (grad ? glu_f32_kernel<true, true> : glu_f32_kernel<false, true>)
                         : (grad ? glu_f32_kernel<true, false> : glu_f32_kernel<false, false>);
     launch_step() = "shared memory size";
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     launch_step() = "gated launch";
     f<<<dim3((unsigned)p.grid, (unsigned)p.nks), kThreads, p.smem, st>>>(
@@ -673,7 +675,7 @@ cudaError_t f32_backward_pair(const void *x, const void *S, const void *A, const
     *parts = p.parts;
     launch_step() = "shared memory size";
     cudaError_t e = cudaFuncSetAttribute(glu_f32_backward_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, p.smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
     launch_step() = "backward launch";
     glu_f32_backward_kernel<<<dim3((unsigned)p.parts, 2), kBackThreads, p.smem, st>>>(

@@ -916,8 +916,11 @@ cudaError_t tc_run(const Plan &pl, const TcArgs &a, Mode mode, cudaStream_t st) 
                     : pl.MP == 64 ? kernel_of<64>(mode)
                                   : kernel_of<128>(mode);
     const size_t smem = (size_t)pl.smem + kTailBytes + 1024;
+    // the limit belongs to the kernel, whoever calls it: the same for all sizes (another host
+    // thread may set it between this one's setting and its launch)
     launch_step() = "shared memory size";
-    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMax + kTailBytes + 1024);
     if (e != cudaSuccess) return e;
     launch_step() = "kernel launch";
     int act = a.activation;

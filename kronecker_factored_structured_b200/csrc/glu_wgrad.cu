@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kCt, kRc == 4 ? 4 : 3) glu_contract_kernel(con
 // and 135; 1 row of 2784 x 3192, r = 2: 123 and 53; 8 rows of 1024 x 1024, r = 4: 57 and 52; 8
 // rows of 1024 x 1280, r = 8: 65 and 59.  At 32 rows dW was faster for all of them.
 constexpr int kSmallRows = 8;
+constexpr int kSmallSmem = 100 * 1024;      // two blocks per SM
 
 struct SmArgs {
     const __nv_bfloat16 *x, *d[2], *S, *A, *B;
@@ -561,7 +562,7 @@ static int ranks_at_a_time(int r) { return r <= 4 ? 4 : 8; }
 WgradPlan wgrad_plan(const Shape &s, int sms) {
     WgradPlan pl{};
     // few rows take the direct kernel, as long as its tiles fit two blocks of shared memory per SM
-    if (s.N <= kSmallRows && small_smem((int)s.N, s.p, s.m1, s.m2, s.r) <= 100 * 1024) {
+    if (s.N <= kSmallRows && small_smem((int)s.N, s.p, s.m1, s.m2, s.r) <= kSmallSmem) {
         pl.direct = 1;
         return pl;
     }
@@ -611,7 +612,7 @@ cudaError_t wgrad_run(const WgradPlan &pl, const void *x, const void *dg, const 
         const size_t smem = small_smem(m.N, s.p, s.m1, s.m2, s.r);
         launch_step() = "shared memory size";
         e = cudaFuncSetAttribute(glu_small_grad_kernel,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallSmem);
         if (e != cudaSuccess) return e;
         launch_step() = "factor-gradient launch";
         const int blocks = m.dc_blocks + m.db_blocks + (dbias ? cdiv(2 * dout, kCt) : 0);

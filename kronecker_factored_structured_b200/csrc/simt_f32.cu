@@ -28,7 +28,10 @@ namespace kron {
 namespace {
 
 constexpr int kThreads = 512;
+// Also the limit of the kernels of run-time sizes, whatever a call's tiles take: the limit is shared
+// by the host threads that call them.
 constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kFwdSmem = kMaxSmem - 16;   // kron_fwd_simt_kernel has 16 bytes besides
 
 // Register-tiled product of shared-memory operands:
 //   Cm(m,n) (+)= sum_{k1<K1, k0<K0} Am(m,k1,k0) * Bm(k1,k0,n)   for every batch b
@@ -924,7 +927,7 @@ BwdLayout bwd_choose(const Shape &s, bool skip) {
 
 int simt_forward_rows(const Shape &s) {
     for (int R : {8, 4, 2, 1})
-        if (fwd_bytes(s, R, false) <= kMaxSmem) return R;
+        if (fwd_bytes(s, R, false) <= kFwdSmem) return R;
     return 0;
 }
 
@@ -958,12 +961,12 @@ cudaError_t simt_forward_t(const void *x, const void *S, const void *A, const vo
         return launch_fwd_f32<F32Cfg<32, 32, 32, 32, 4, 8>, TI>(x, S, A, B, bias, y, s, st);
     int R = simt_forward_rows(s);
     // the skip lists need room too; rows of a tile are independent, so R may shrink
-    while (skip && R > 1 && fwd_bytes(s, R, true) > kMaxSmem) R >>= 1;
-    if (skip && fwd_bytes(s, R, true) > kMaxSmem) skip = false;
+    while (skip && R > 1 && fwd_bytes(s, R, true) > kFwdSmem) R >>= 1;
+    if (skip && fwd_bytes(s, R, true) > kFwdSmem) skip = false;
     const FwdLayout L = fwd_layout(s, R, skip);
     const size_t smem = L.total * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(kron_fwd_simt_kernel<TI>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwdSmem);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (s.N + R - 1) / R;
     cudaLaunchConfig_t cfg = {};
@@ -1006,7 +1009,7 @@ cudaError_t simt_backward_t(const void *x, const void *S, const void *A, const v
     const BwdLayout L = bwd_choose(s, skip);
     const size_t smem = L.total * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(kron_bwd_simt_kernel<TI>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e != cudaSuccess) return e;
     const int64_t rows_per_part = (s.N + parts - 1) / parts;
     cudaLaunchConfig_t cfg = {};
@@ -1040,7 +1043,7 @@ cudaError_t simt_backward_pair(const void *x, const void *S, const void *A, cons
     const size_t smem = L.total * sizeof(float);
     launch_step() = "shared memory size";
     cudaError_t e = cudaFuncSetAttribute(kron_bwd_simt_kernel<float>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
     if (e != cudaSuccess) return e;
     const int64_t rows_per_part = (s.N + parts - 1) / parts;
     launch_step() = "backward launch";

@@ -8,7 +8,9 @@ gate and of up, d, V, C again, the output), the gate's two times the activation'
 number, at most 1.4 in the mean square over these inputs: sqrt(6 + 2 * 1.96) 2^-8 / sqrt(3) =
 7.1e-3 for sums of terms of random sign.  8e-3 leaves a tenth for the sample.  Exact FP32:
 1e-5 of the largest value, as for the layer."""
+import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -437,3 +439,75 @@ def test_tails_of_the_activations(name, dtype):
     # of one row: the column sum is dg itself
     err, tol = (out["dbias"][0].double().cpu() - df).abs(), fn * terms + half * df.abs() + low
     assert bool((err <= tol).all()), g[err > tol]
+
+
+# dtype, and two sizes (N, p, q, m1, m2, r) that run the same instantiations of the kernels with
+# tiles of different size: the kernels on the tensor cores, the factor gradients of few rows, the
+# exact-FP32 kernels, and the layer's FP32 backward beside a gated one that runs its kernel
+THREADS = [("bf16", (300, 32, 32, 32, 32, 4), (300, 2, 2, 32, 32, 1)),
+           ("bf16", (8, 300, 2, 8, 8, 1), (8, 4, 4, 8, 8, 1)),
+           ("f32", (37, 30, 22, 12, 20, 2), (5, 2, 2, 4, 4, 1)),
+           ("f32", (9, 4, 4, 64, 64, 8), (5, 2, 2, 8, 8, 1))]
+
+
+@pytest.mark.parametrize("case", range(4), ids=["bf16", "bf16_few_rows", "f32", "f32_layer"])
+def test_host_threads_at_once(case):
+    """Calls of two sizes from several host threads, which meet inside the library: every one
+    succeeds, and gives what it gives alone."""
+    dtype, *sizes = THREADS[case]
+    lib = native.load()
+
+    def setup(k):
+        N, *shape = sizes[k]
+        d = make(N, *shape, dtype=dtype, seed=k)
+        fac = [d[n] for n in ("x", "S", "A", "B")]
+        stream = torch.cuda.Stream()
+        p, q, m1, m2, r = shape
+        tail = (N, p, q, m1, m2, r)
+        if case == 3 and k == 1:      # the layer
+            fac[1:] = [t[0].contiguous() for t in fac[1:]]
+            want = kfs.backward(*fac, d["dH"], dtype=dtype)
+            n = kfs.workspace_size(*tail, dtype)
+        else:
+            want = native.glu_backward(*fac, d["dH"], d["bias"], dtype=dtype)
+            want["h"] = native.glu_forward(*fac, d["bias"], dtype=dtype)
+            n = native.glu_workspace_size(*tail, dtype, True)
+        out = {n: torch.zeros_like(v) for n, v in want.items()}
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device=DEV)
+        P = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+        fp = [P(t) for t in fac]
+        grads = [P(out[n]) for n in ("dX", "dS", "dA", "dB", "dbias")]
+        end = (native.DTYPES[dtype], 0, P(ws), ws.numel(), ctypes.c_void_p(stream.cuda_stream))
+        if case == 3 and k == 1:
+            calls = [(lib.kron_linear_backward, (*fp, P(d["dH"]), *grads, *tail, *end))]
+        else:
+            bias = P(d["bias"])
+            calls = [(lib.kron_glu_forward, (*fp, bias, P(out["h"]), *tail, 0, *end)),
+                     (lib.kron_glu_backward, (*fp, bias, P(d["dH"]), *grads, *tail, 0, *end))]
+        return want, out, calls, stream, (d, fac, ws)
+
+    work = [setup(k) for k in (0, 1, 0, 1, 0, 1)]
+    torch.cuda.synchronize()
+    failed = []
+    start = threading.Barrier(len(work))
+
+    def loop(i):
+        _, _, calls, stream, _ = work[i]
+        start.wait()
+        for n in range(2000):
+            for f, args in calls:
+                if f(*args):
+                    failed.append(lib.kron_last_error().decode())
+            if n % 100 == 99:
+                stream.synchronize()
+
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, (len(failed), failed[:3])
+    for want, out, *_ in work:
+        for n in want:
+            assert torch.equal(out[n], want[n]), n
