@@ -260,12 +260,18 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
  *   x, dX [N][p*m1];  h, dH [N][q*m2]
  * `activation` is a kron_activation_t.  flags must be 0.
  *   KRON_F32   every tensor float32, exact FP32 arithmetic on the CUDA cores; m1 and m2
- *              multiples of 4
+ *              multiples of 4, and a row's tile has to fit shared memory, else
+ *              KRON_ERR_UNSUPPORTED
  *   KRON_BF16  every tensor bfloat16, the gradients too (each rounded once from float32);
  *              tcgen05 tensor cores: both projections, the activation and the product in one
  *              kernel.  Sizes are run-time values; m1 and m2 multiples of 8 up to 256, p and q
  *              at most 1024, and the factors of some slice of the layer have to fit shared
- *              memory, else KRON_ERR_UNSUPPORTED (about r p <= 1000 and r m1 <= 2000)
+ *              memory, else KRON_ERR_UNSUPPORTED.  With |p| = p rounded up to a multiple of 16 and
+ *              |m| = m rounded up to 16, 32 or a multiple of 64, they do for
+ *                  ceil(r / 4) (|p| + |m1|) + 2 |m1| <= 646,
+ *              and for the backward, which forms dX with the roles swapped, where also
+ *                  2 ceil(r / 8) (|q| + |m2|) + 2 |m2| <= 646,
+ *              and for some larger ones
  *   KRON_TF32  KRON_ERR_UNSUPPORTED
  * Backward: gradients of <dH, h>; the pre-activations are formed again, nothing is kept from
  * the forward call.  bias may be NULL (none); dX and dbias may be NULL (skipped).  On KRON_BF16
@@ -277,7 +283,9 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
  * `workspace`: kron_glu_workspace_size(..., backward) bytes, 256-byte aligned, owned by the
  * caller; two calls that may run at the same time need one each.  The forward needs 0 bytes
  * (workspace may then be NULL), but for some shapes and many rows in KRON_F32.  0 also means
- * arguments that the call refuses.  N <= 2^30.
+ * arguments that the call refuses, and for the backward with N > 0 only that; whether the forward
+ * has a kernel for a shape, a call with N = 0 tells without launching anything.  A backward that is
+ * refused does not keep the forward from running.  N <= 2^30.
  * Results are bitwise reproducible on one GPU model.  Everything else as for the layer.
  */
 typedef enum {

@@ -93,7 +93,7 @@ unsigned grid_for(int64_t n4) {
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int activation,
-                          kron_dtype_t dtype, unsigned flags) {
+                          kron_dtype_t dtype, unsigned flags, bool backward) {
     report_failure(KRON_OK, "");
     if (dtype != KRON_F32 && dtype != KRON_TF32 && dtype != KRON_BF16)
         return bad(KRON_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
@@ -115,17 +115,19 @@ kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int ac
     const Shape s{N > 0 ? N : 1, p, q, m1, m2, r};
     Plan pl;
     if (dtype == KRON_BF16) {
-        if (p > 1024 || q > 1024 || m1 > 256 || m2 > 256 ||
-            !glu::tc_plan(&pl, s, glu::kForward, kRowParts) ||
-            !glu::tc_plan(&pl, s, glu::kInput, kRowParts))
-            return bad(KRON_ERR_UNSUPPORTED,
-                       "no tensor-core kernel for p=%d q=%d m1=%d m2=%d r=%d: blocks above 256 or "
-                       "factors that do not fit shared memory (KRON_F32 runs any shape)",
-                       p, q, m1, m2, r);
-    } else if (simt_forward_rows(s) <= 0 || simt_backward_rows(s) <= 0) {
+        if (p > 1024 || q > 1024 || m1 > 256 || m2 > 256)
+            return bad(KRON_ERR_UNSUPPORTED, "KRON_BF16 takes p and q up to 1024 and m1 and m2 up to "
+                       "256 (got p=%d q=%d m1=%d m2=%d)", p, q, m1, m2);
+        if (!glu::tc_plan(&pl, s, glu::kForward, kRowParts))
+            return bad(KRON_ERR_UNSUPPORTED, "no tensor-core kernel for p=%d q=%d m1=%d m2=%d r=%d: "
+                       "too large r (p + m1) for shared memory", p, q, m1, m2, r);
+        if (backward && !glu::tc_plan(&pl, s, glu::kInput, kRowParts))
+            return bad(KRON_ERR_UNSUPPORTED, "no tensor-core kernel for the gradients of p=%d q=%d "
+                       "m1=%d m2=%d r=%d: too large r (q + m2) for shared memory", p, q, m1, m2, r);
+    } else if (simt_forward_rows(s) <= 0 || (backward && simt_backward_rows(s) <= 0)) {
         return bad(KRON_ERR_UNSUPPORTED,
-                   "no kernel for p=%d q=%d m1=%d m2=%d r=%d: the FP32 tile does not fit shared "
-                   "memory", p, q, m1, m2, r);
+                   "no %s kernel for p=%d q=%d m1=%d m2=%d r=%d: the FP32 tile does not fit shared "
+                   "memory", backward ? "backward" : "forward", p, q, m1, m2, r);
     }
     return KRON_OK;
 }
@@ -190,7 +192,8 @@ extern "C" {
 
 size_t kron_glu_workspace_size(int64_t N, int p, int q, int m1, int m2, int r, kron_dtype_t dtype,
                                int backward) {
-    if (check_sizes(N, p, q, m1, m2, r, KRON_ACT_SILU, dtype, 0) != KRON_OK || N == 0) return 0;
+    if (check_sizes(N, p, q, m1, m2, r, KRON_ACT_SILU, dtype, 0, backward != 0) != KRON_OK || N == 0)
+        return 0;
     return need_bytes(Shape{N, p, q, m1, m2, r}, dtype, backward != 0);
 }
 
@@ -198,7 +201,7 @@ kron_status_t kron_glu_forward(const void *x, const void *S, const void *A, cons
                                const void *bias, void *h, int64_t N, int p, int q, int m1, int m2,
                                int r, int activation, kron_dtype_t dtype, unsigned flags,
                                void *workspace, size_t workspace_bytes, void *stream) {
-    kron_status_t st = check_sizes(N, p, q, m1, m2, r, activation, dtype, flags);
+    kron_status_t st = check_sizes(N, p, q, m1, m2, r, activation, dtype, flags, false);
     if (st != KRON_OK) return st;
     if (!S || !A || !B || (N > 0 && (!x || !h)))
         return bad(KRON_ERR_INVALID_ARG, "S, A, B (and x, h when N > 0) must be non-null");
@@ -246,7 +249,7 @@ kron_status_t kron_glu_backward(const void *x, const void *S, const void *A, con
                                 void *dB, void *dbias, int64_t N, int p, int q, int m1, int m2,
                                 int r, int activation, kron_dtype_t dtype, unsigned flags,
                                 void *workspace, size_t workspace_bytes, void *stream) {
-    kron_status_t st = check_sizes(N, p, q, m1, m2, r, activation, dtype, flags);
+    kron_status_t st = check_sizes(N, p, q, m1, m2, r, activation, dtype, flags, true);
     if (st != KRON_OK) return st;
     if (!S || !A || !B || !dS || !dA || !dB || (N > 0 && (!x || !dH)))
         return bad(KRON_ERR_INVALID_ARG,

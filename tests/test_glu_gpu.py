@@ -511,3 +511,14 @@ def test_host_threads_at_once(case):
     for want, out, *_ in work:
         for n in want:
             assert torch.equal(out[n], want[n]), n
+
+
+def test_forward_without_a_backward():
+    """Sizes whose forward has a kernel and whose gradients have none."""
+    for dtype, N, shape in (("bf16", 37, (64, 224, 64, 64, 8)), ("f32", 9, (128, 128, 64, 64, 1))):
+        d = make(N, *shape, dtype=dtype, seed=5)
+        fac = (d["x"], d["S"], d["A"], d["B"])
+        ref = reference({k: v for k, v in d.items() if k != "dH"}, "silu")
+        compare({"h": native.glu_forward(*fac, d["bias"], dtype=dtype)}, ref, dtype)
+        with pytest.raises(native.KronError):
+            native.glu_backward(*fac, d["dH"], d["bias"], dtype=dtype)

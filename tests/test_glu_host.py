@@ -106,3 +106,45 @@ def test_binding_rejects():
         kfs.KronGLU(96, 96, 32, activation="relu")
     with pytest.raises(ValueError):
         kfs.KronGLU(96, 100, 32)
+
+
+def _up(v, n):
+    return -(-v // n) * n
+
+
+def test_documented_limits_of_bf16():
+    """Every size within the header's inequalities has a kernel, and the forward does not ask for
+    the backward's."""
+    pad = lambda m: 16 if m <= 16 else 32 if m <= 32 else _up(m, 64)  # noqa: E731
+    takes = {False: 0, True: 0}
+    for p in (1, 7, 16, 33, 64, 200, 256, 700, 1024):
+        for q in (1, 16, 33, 64, 224, 1024):
+            for m1 in (8, 24, 64, 160, 256):
+                for m2 in (8, 40, 64, 256):
+                    for r in (1, 2, 4, 5, 8, 16, 24):
+                        fwd = -(-r // 4) * (_up(p, 16) + pad(m1)) + 2 * pad(m1) <= 646
+                        bwd = 2 * -(-r // 8) * (_up(q, 16) + pad(m2)) + 2 * pad(m2) <= 646
+                        size = dict(p=p, q=q, m1=m1, m2=m2, r=r)
+                        if fwd:       # accepted: with no rows there is nothing to launch
+                            assert call(False, N=0, **size) == 0, size
+                            takes[False] += 1
+                        if fwd and bwd:
+                            assert native.glu_workspace_size(8, **size, dtype="bf16",
+                                                             backward=True) > 0, size
+                            takes[True] += 1
+    assert takes[False] > takes[True] > 500
+
+
+def test_forward_where_the_backward_has_no_kernel():
+    """4096 -> 14336, blocks of 64, eight ranks: dX does not fit, the forward does."""
+    size = dict(p=64, q=224, m1=64, m2=64, r=8)
+    assert call(False, x=None, **size) == 1          # past the sizes, to the pointers
+    assert call(False, N=0, **size) == 0
+    assert call(True, **size) == 2
+    assert "gradients" in native.load().kron_last_error().decode()
+    assert native.glu_workspace_size(8, **size, dtype="bf16", backward=True) == 0
+    # FP32: a row's tile of the backward has more in it
+    size = dict(p=128, q=128, m1=64, m2=64, r=1)
+    assert call(False, N=0, dtype=0, **size) == 0
+    assert call(True, dtype=0, **size) == 2
+    assert native.glu_workspace_size(8, **size, dtype="f32", backward=True) == 0
