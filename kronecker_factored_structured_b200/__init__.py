@@ -192,12 +192,20 @@ class KronGLU(torch.nn.Module):
 
 class KronGatedFFN(torch.nn.Module):
     """Gated feed-forward block of Kronecker-factored projections: ``KronGLU`` (``glu``) to the
-    hidden width, ``KronLinear`` (``down``) back, whose shapes and dtypes are its own."""
+    hidden width, ``KronLinear`` (``down``) back, whose shapes and dtypes are its own.  "f32" takes
+    run-time sizes; in "bf16" ``down`` has kernels for the layer's compiled shapes only, and other
+    sizes are refused here (ValueError): put a ``KronGLU`` before a projection of your own."""
 
     def __init__(self, features, hidden_features, block, hidden_block=None, rank=1, bias=True,
                  activation="silu", dtype="bf16", device=None):
         super().__init__()
         hidden_block = block if hidden_block is None else hidden_block
+        if dtype == "bf16" and not (features % block or hidden_features % hidden_block):
+            down = (hidden_features // hidden_block, features // block, hidden_block, block, rank)
+            if not native.workspace_size(1, *down, dtype):
+                raise ValueError(
+                    "no bf16 kernel for the projection back: p=%d q=%d m1=%d m2=%d r=%d is not one "
+                    "of the layer's compiled shapes (dtype='f32' takes run-time sizes)" % down)
         self.glu = KronGLU(features, hidden_features, block, hidden_block, rank, bias, activation,
                            dtype, device)
         self.down = KronLinear(hidden_features, features, hidden_block, block, rank, bias, dtype,

@@ -148,3 +148,18 @@ def test_forward_where_the_backward_has_no_kernel():
     assert call(False, N=0, dtype=0, **size) == 0
     assert call(True, dtype=0, **size) == 2
     assert native.glu_workspace_size(8, **size, dtype="f32", backward=True) == 0
+
+
+def test_gated_block_refuses_sizes_that_its_projection_back_lacks():
+    """In BF16 the layer has kernels for compiled shapes only: said at construction, not by the
+    first forward."""
+    for sizes in ((768, 2048, 32, 64, 1), (1024, 1024, 32, 32, 2), (96, 160, 16, 32, 2)):
+        *sizes, rank = sizes
+        with pytest.raises(ValueError, match="projection back"):
+            kfs.KronGatedFFN(*sizes, rank=rank, dtype="bf16")
+        kfs.KronGatedFFN(*sizes, rank=rank, dtype="f32")
+        kfs.KronGLU(*sizes, rank=rank, dtype="bf16")
+    kfs.KronGatedFFN(1024, 1024, 32, rank=4, dtype="bf16")
+    kfs.KronGatedFFN(4096, 4096, 64, rank=8, dtype="bf16")
+    with pytest.raises(ValueError):
+        kfs.KronGatedFFN(768, 2000, 32, 64, dtype="bf16")
