@@ -250,7 +250,7 @@ def distill_loss(logits, values, indices, labels=None, weights=None, temperature
 
     ``values`` (float32) and ``indices`` hold the teacher's logits of each row and their
     columns, an index outside the vocabulary being no entry; shapes are (..., V), (..., K) and
-    (...).  ``weights`` multiplies the rows.  reduction: "none" (the rows' losses), "sum", or
+    (...), of any strides (logits whose rows are not contiguous are copied).  ``weights`` multiplies the rows.  reduction: "none" (the rows' losses), "sum", or
     "mean" (the sum over the sum of ``weights``, or over the rows without them).  ``logits`` and
     ``weights`` are differentiable (the backward forms the rows' losses again for the weights);
     the teacher gets no gradient.
@@ -260,8 +260,12 @@ def distill_loss(logits, values, indices, labels=None, weights=None, temperature
     lead = logits.shape[:-1]
     flat = lambda t: None if t is None else t.reshape(-1).contiguous()  # noqa: E731
     weights = flat(weights)
+    rows = logits.reshape(-1, logits.shape[-1])
+    # rows may lie further apart than their length; anything else is copied
+    if rows.stride(1) != 1 or (len(rows) > 1 and rows.stride(0) < rows.shape[1]):
+        rows = rows.contiguous()
     loss = DistillFunction.apply(
-        logits.reshape(-1, logits.shape[-1]), values.reshape(-1, values.shape[-1]).contiguous(),
+        rows, values.reshape(-1, values.shape[-1]).contiguous(),
         indices.reshape(-1, indices.shape[-1]).contiguous(), flat(labels), weights,
         float(temperature), float(label_weight))
     if reduction == "none":

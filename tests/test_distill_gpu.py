@@ -467,3 +467,22 @@ def test_extreme_temperatures(tau):
         lse = native.distill_forward(*args, **kw)["lse"]
         eps += 1.5 * 1024 * 2.0 ** -24
         check_grad(native.distill_backward(*args, lse, **kw), grad, size * eps / EPS, torch.float32)
+
+
+def test_logits_of_any_layout():
+    """Transposed and broadcast logits, as any strided tensor of another operand."""
+    d = make(6, 257, 8, torch.float32, seed=20, holes=False)
+    args = (d["values"], d["indices"], d["labels"], d["weights"])
+    kw = dict(temperature=2.0, label_weight=0.3, reduction="sum")
+    z = d["logits"].clone().requires_grad_(True)
+    (want,) = torch.autograd.grad(kfs.distill_loss(z, *args, **kw), z)
+    t = d["logits"].t().contiguous().requires_grad_(True)
+    (got,) = torch.autograd.grad(kfs.distill_loss(t.t(), *args, **kw), t)
+    assert torch.equal(got.t(), want)
+    one = d["logits"][:1].clone().requires_grad_(True)
+    rows = d["logits"][:1].expand(6, 257).contiguous().requires_grad_(True)
+    (want,) = torch.autograd.grad(kfs.distill_loss(rows, *args, **kw), rows)
+    (got,) = torch.autograd.grad(kfs.distill_loss(one.expand(6, 257), *args, **kw), one)
+    # the broadcast's gradient is the sum of six rows
+    assert float((got - want.sum(0, keepdim=True)).abs().max()) <= 8 * 2.0 ** -24 * float(
+        want.abs().sum(0).max())
