@@ -449,6 +449,8 @@ def _glu_workspace(sizes, dtype, backward, workspace, dev):
         workspace = torch.empty(n, dtype=torch.uint8, device=dev)
     elif workspace.device != dev:
         raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

@@ -163,3 +163,16 @@ def test_gated_block_refuses_sizes_that_its_projection_back_lacks():
     kfs.KronGatedFFN(4096, 4096, 64, rank=8, dtype="bf16")
     with pytest.raises(ValueError):
         kfs.KronGatedFFN(768, 2000, 32, 64, dtype="bf16")
+
+
+def test_binding_rejects_a_workspace_that_is_smaller_than_it_looks():
+    """A broadcast buffer has as many elements as a real one and no memory behind them."""
+    cpu = torch.device("cpu")
+    size = (8, 4, 4, 16, 16, 2)
+    n = native.glu_workspace_size(*size, "bf16", True)
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(n), torch.empty(2 * n).view(n, 2)[:, 0]):
+        with pytest.raises(ValueError, match="contiguous"):
+            native._glu_workspace(size, "bf16", True, bad, cpu)
+    good = torch.empty(n // 4 + 1)
+    _, at, nbytes = native._glu_workspace(size, "bf16", True, good, cpu)
+    assert at == good.data_ptr() and nbytes == 4 * good.numel()
