@@ -384,6 +384,8 @@ def _on_device(dev, stream):
     """Context in which dev is the current device, and memory that is allocated belongs to the
     stream that the call runs on (a workspace may be handed out again once it returns)."""
     if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
         return torch.cuda.stream(stream)
     return _NOTHING if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 

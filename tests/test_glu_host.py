@@ -176,3 +176,12 @@ def test_binding_rejects_a_workspace_that_is_smaller_than_it_looks():
     good = torch.empty(n // 4 + 1)
     _, at, nbytes = native._glu_workspace(size, "bf16", True, good, cpu)
     assert at == good.data_ptr() and nbytes == 4 * good.numel()
+
+
+def test_binding_rejects_a_stream_of_another_device():
+    """The kernels would run on the stream's GPU with pointers of another one."""
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+    with pytest.raises(ValueError, match="stream"):
+        native._on_device(torch.device("cuda", 0), Stream())
