@@ -339,8 +339,9 @@ KRON_API kron_status_t kron_glu_backward(const void *x, const void *S, const voi
  *   dlogits rows ld_out elements apart, of the logits' type; may be the logits themselves
  *           (the same pointer and stride), and does not overlap them otherwise
  *   0.05 <= temperature <= 1e3, 0 <= label_weight <= 1
- * kron_distill_step gives `loss` and the `dlogits` of the sum of `loss` in one call, reading
- * the logits from memory once.  Sums are formed in float32 in a fixed order: results are bitwise
+ * kron_distill_step gives `loss` and the `dlogits` of the sum of `loss` in one call.  It reads
+ * every row twice, the second time from L2 where the rows at work at a time (up to 740) fit
+ * there.  Sums are formed in float32 in a fixed order: results are bitwise
  * reproducible.  No workspace.  Tensors need the alignment of their elements; rows that are
  * also 16-byte aligned alike in logits and dlogits are stored 16 bytes at a time.  Everything
  * else as for the layer above.

@@ -31,7 +31,8 @@ from .native import KronError, backward, forward, workspace_size
 
 __all__ = ["native", "accounting", "forward", "backward", "workspace_size", "KronError",
            "KronLinearFunction", "KronLinear", "kron_linear", "KSLinearFunction", "KSLinear",
-           "ks_linear", "KronGLUFunction", "KronGLU", "kron_glu", "KronGatedFFN", "DistillFunction", "DistillLoss", "distill_loss"]
+           "ks_linear", "KronGLUFunction", "KronGLU", "kron_glu", "KronGatedFFN",
+           "DistillFunction", "DistillLoss", "distill_loss"]
 
 
 class KronLinearFunction(torch.autograd.Function):
@@ -250,10 +251,11 @@ def distill_loss(logits, values, indices, labels=None, weights=None, temperature
 
     ``values`` (float32) and ``indices`` hold the teacher's logits of each row and their
     columns, an index outside the vocabulary being no entry; shapes are (..., V), (..., K) and
-    (...), of any strides (logits whose rows are not contiguous are copied).  ``weights`` multiplies the rows.  reduction: "none" (the rows' losses), "sum", or
-    "mean" (the sum over the sum of ``weights``, or over the rows without them).  ``logits`` and
-    ``weights`` are differentiable (the backward forms the rows' losses again for the weights);
-    the teacher gets no gradient.
+    (...), of any strides (logits whose rows are not contiguous are copied).  ``weights``
+    multiplies the rows.  reduction: "none" (the rows' losses), "sum", or "mean" (the sum over the
+    sum of ``weights``, or over the rows without them).  ``logits`` and ``weights`` are
+    differentiable (the backward forms the rows' losses again for the weights); the teacher gets
+    no gradient.
     """
     if reduction not in ("none", "sum", "mean"):
         raise ValueError(f"reduction must be 'none', 'sum' or 'mean', got {reduction!r}")

@@ -6,17 +6,20 @@
 //   loss = w [ (1 - lam) tau^2 sum_j p_j (log p_j - log q_{i_j}) + lam (lse(x) - x_label) ]
 //   dx_v = w dl [ (1 - lam) tau (q_v - sum_{j: i_j = v} p_j) + lam (softmax(x)_v - [v = label]) ]
 //
-// One CTA of 256 threads per row, five or six per SM (more threads where there are few rows).  Pass
-// 1 reads the row with a running maximum m per thread and the sums of exp((x - m)/tau) and
-// exp(x - m); pass 2 (gradient) reads it again and writes the dense part c_t q + c_1 softmax(x); the
-// K + 1 columns that the teacher and the label touch are then overwritten by the thread that owns
-// the first entry of the column, in fp32, from logits fetched before anything is written (so dlogits
-// may be the logits).  Exponents are differences from a value next to the maximum, never from zero.
+// One CTA of 256 threads per row, five or six per SM (more threads where there are few rows).
+// Pass 1 reads the row with a running maximum m per thread and the sums of exp((x - m)/tau) and
+// exp(x - m); pass 2 (gradient) reads it again, from L2 where the rows at work fit there, and
+// writes the dense part c_t q + c_1 softmax(x); the K + 1 columns that the teacher and the label
+// touch are then overwritten by the thread that owns the first entry of the column, in fp32, from
+// logits fetched before anything is written (so dlogits may be the logits).  Exponents are
+// differences from a value next to the row's maximum, however far from zero the logits are.
 // Bound: HBM moves the logits once in and once out (126 us for 4096 x 50257 bf16); per element
 // and pass one ex2 (two for a tau other than 1, 2 and 4), 92 us on the special-function units,
-// and with the packed FP32 instructions some 11 issue slots.  Measured 177 us (scalar FP32
-// instructions: 191; 512 threads, three CTAs per SM: 212; rows split over clusters of four
-// CTAs and held in registers, one read: 301, the barriers of the shorter pieces not covered).
+// and with the packed FP32 instructions some 11 issue slots.  Measured FIGSTEP (an earlier form
+// with six CTAs per SM 181; with scalar FP32 instructions 191; 512 threads, three CTAs per SM:
+// 212; rows split over clusters of four CTAs and held in registers, one read: 301, the barriers
+// of the shorter pieces not covered).  740 rows at work exceed L2 where a row has more than 170
+// KB: 1024 x 50257 fp32 read 333 MB for 206, 1024 x 131072 bf16 462 for 268.
 #include "../../include/kron_linear.h"
 #include "internal.h"
 #include "packed.cuh"
@@ -215,10 +218,12 @@ struct Origin {
 __device__ __forceinline__ Origin origin_of(float m, float lsum_t, float lsum_1) {
     return {m, -lsum_t, -lsum_1};
 }
-// From the log-sum-exps, in 64 bits: no error but theirs.  With one exponential only the one at its
-// temperature is known.
-template <int E> __device__ __forceinline__ Origin origin_of(const float *lse, float tau, bool hard) {
-    const float lse_t = hard ? lse[1] : lse[0], at = E == kOne ? (float)((double)lse_t * tau) : lse[1];
+// From the log-sum-exps, in 64 bits: no error but theirs.  With one exponential only the one at
+// its temperature is known.
+template <int E>
+__device__ __forceinline__ Origin origin_of(const float *lse, float tau, bool hard) {
+    const float lse_t = hard ? lse[1] : lse[0];
+    const float at = E == kOne ? (float)((double)lse_t * tau) : lse[1];
     const float t = (float)((double)at / tau - lse_t);
     return {at, t, E == kOne ? t : 0.f};
 }
@@ -247,8 +252,8 @@ __device__ __forceinline__ Stat block_stat(Stat st, float a, Stat *warp) {
 template <int E> struct Dense {
     f2 a, b, ct, c1, b1;
     // Whether (x - at) a is formed as one multiply-add x a + b whose rounded constant the
-    // coefficients make up for; else the caller subtracts `at` first (a fourth instruction in packed
-    // arithmetic, which took 197 us instead of 181 for 4096 x 50257 bf16, tau = 2, with the loss).
+    // coefficients make up for; else the caller subtracts `at` first (a fourth instruction in
+    // packed arithmetic: 197 us instead of 188 for 4096 x 50257 bf16, tau = 2, with the loss).
     static __device__ __forceinline__ bool is_near(const Origin &o, float scale) {
         return fabsf(o.at * scale) <= 0x1p24f && (E != kTwo || fabsf(o.at * kLog2e) <= 0x1p24f);
     }
@@ -257,9 +262,11 @@ template <int E> struct Dense {
         const bool near = is_near(o, scale);
         const float bt = near ? -o.at * scale : 0.f, bo = near ? -o.at * kLog2e : 0.f;
         // what is left of at a + b, at most 1
-        const float rt = near ? fmaf(o.at, scale, bt) : 0.f, ro = near ? fmaf(o.at, kLog2e, bo) : 0.f;
+        const float rt = near ? fmaf(o.at, scale, bt) : 0.f;
+        const float ro = near ? fmaf(o.at, kLog2e, bo) : 0.f;
         const float r1 = E == kSquare ? 2.f * rt : E == kFourth ? 4.f * rt : E == kTwo ? ro : rt;
-        const float ft = soft * ex2(fmaf(o.t, kLog2e, -rt)), f1 = hard * ex2(fmaf(o.one, kLog2e, -r1));
+        const float ft = soft * ex2(fmaf(o.t, kLog2e, -rt));
+        const float f1 = hard * ex2(fmaf(o.one, kLog2e, -r1));
         a = dup2(scale);
         b = dup2(bt);
         b1 = dup2(bo);
@@ -402,8 +409,8 @@ __global__ void __launch_bounds__(32 * kShortWarps) distill_short_kernel(const A
     }
 }
 
-// A row's sums formed again by a gradient, for log-sum-exps that are too far from zero.  A call: its
-// registers are not the gradient's.
+// A row's sums formed again by a gradient, for log-sum-exps that are too far from zero.  A call,
+// whose registers are not the gradient's (inlined: 157 -> 168 us for 4096 x 50257 bf16).
 template <typename T, int E, int kThreads>
 __device__ __noinline__ Origin far_origin(const T *x, int V, float a, Stat *warp) {
     Stat st{-INFINITY, 0.f, 0.f};
@@ -413,9 +420,9 @@ __device__ __noinline__ Origin far_origin(const T *x, int V, float a, Stat *warp
     return origin_of(r.m, lsum, E == kOne ? lsum : logf(r.s1));
 }
 
-// Threads per SM for which registers are set aside.  Loss and gradient in one kernel take five CTAs of
-// 256 threads (48 registers) rather than six (40): 4096 x 50257 bf16 at tau = 1, 2 and 4 183, 188 and
-// 195 us and 192, 188 and 191; 1023 x 32000 38, 39 and 41 us and 42, 41 and 43.
+// Threads per SM for which registers are set aside.  Loss and gradient in one kernel take five
+// CTAs of 256 threads (48 registers) rather than six (40): 4096 x 50257 bf16 at tau = 1, 2 and 4
+// took 183, 188 and 195 us and 192, 188 and 191; 1023 x 32000 38, 39 and 41 and 42, 41 and 43.
 constexpr int threads_per_sm(bool stats, bool grad, int threads) {
     return !stats ? 2048 : grad && threads == 256 ? 1280 : 1536;
 }
@@ -640,7 +647,8 @@ distill_kernel(const Args g) {
         const int tail = head + nv * n + tid;
         if (tail < V) Vc::put(out + tail, dense.one(Vc::get(x + tail)));
     } else {
-        for (int v = tid; v < V; v += kThreads) Vc::put(out + v, dense.one(Vc::get(x + v) - last.at));
+        for (int v = tid; v < V; v += kThreads)
+            Vc::put(out + v, dense.one(Vc::get(x + v) - last.at));
     }
     __syncthreads();
     // with the loss in the same kernel there are no registers to keep these over the dense pass

@@ -116,14 +116,17 @@ kron_status_t check_sizes(int64_t N, int p, int q, int m1, int m2, int r, int ac
     Plan pl;
     if (dtype == KRON_BF16) {
         if (p > 1024 || q > 1024 || m1 > 256 || m2 > 256)
-            return bad(KRON_ERR_UNSUPPORTED, "KRON_BF16 takes p and q up to 1024 and m1 and m2 up to "
-                       "256 (got p=%d q=%d m1=%d m2=%d)", p, q, m1, m2);
+            return bad(KRON_ERR_UNSUPPORTED,
+                       "KRON_BF16 takes p and q up to 1024 and m1 and m2 up to 256 (got p=%d q=%d "
+                       "m1=%d m2=%d)", p, q, m1, m2);
         if (!glu::tc_plan(&pl, s, glu::kForward, kRowParts))
-            return bad(KRON_ERR_UNSUPPORTED, "no tensor-core kernel for p=%d q=%d m1=%d m2=%d r=%d: "
-                       "too large r (p + m1) for shared memory", p, q, m1, m2, r);
+            return bad(KRON_ERR_UNSUPPORTED,
+                       "no tensor-core kernel for p=%d q=%d m1=%d m2=%d r=%d: too large r (p + m1) "
+                       "for shared memory", p, q, m1, m2, r);
         if (backward && !glu::tc_plan(&pl, s, glu::kInput, kRowParts))
-            return bad(KRON_ERR_UNSUPPORTED, "no tensor-core kernel for the gradients of p=%d q=%d "
-                       "m1=%d m2=%d r=%d: too large r (q + m2) for shared memory", p, q, m1, m2, r);
+            return bad(KRON_ERR_UNSUPPORTED,
+                       "no tensor-core kernel for the gradients of p=%d q=%d m1=%d m2=%d r=%d: too "
+                       "large r (q + m2) for shared memory", p, q, m1, m2, r);
     } else if (simt_forward_rows(s) <= 0 || (backward && simt_backward_rows(s) <= 0)) {
         return bad(KRON_ERR_UNSUPPORTED,
                    "no %s kernel for p=%d q=%d m1=%d m2=%d r=%d: the FP32 tile does not fit shared "
@@ -192,7 +195,8 @@ extern "C" {
 
 size_t kron_glu_workspace_size(int64_t N, int p, int q, int m1, int m2, int r, kron_dtype_t dtype,
                                int backward) {
-    if (check_sizes(N, p, q, m1, m2, r, KRON_ACT_SILU, dtype, 0, backward != 0) != KRON_OK || N == 0)
+    const bool back = backward != 0;
+    if (check_sizes(N, p, q, m1, m2, r, KRON_ACT_SILU, dtype, 0, back) != KRON_OK || N == 0)
         return 0;
     return need_bytes(Shape{N, p, q, m1, m2, r}, dtype, backward != 0);
 }

@@ -121,10 +121,10 @@ __device__ __forceinline__ f2 sigmoid2(f2 g) {
 }
 
 // (1 + erf(g / sqrt 2)) / 2, e = exp(-g^2 / 2): the lower tail as e times a polynomial in 1 / (1 +
-// 0.31 |g|), a minimax fit of degree 6 without constant term, 2^-17.6 of the tail for |g| <= 14, where
-// e vanishes; the upper one is 1 less that, and neither cancels.  (Scalar: in packed arithmetic gelu
-// took 48 us instead of 49 for 20000 x 1024, r = 4, but silu, in the same kernel, 45.7 instead of
-// 43.6.  erff: 55, and nothing left of the value below g = -5.)
+// 0.31 |g|), a minimax fit of degree 6 without constant term, 2^-17.6 of the tail for |g| <= 14,
+// where e vanishes; the upper one is 1 less that, and neither cancels.  (Scalar: in packed
+// arithmetic gelu took 48 us instead of 49 for 20000 x 1024, r = 4, but silu, in the same kernel,
+// 45.7 instead of 43.6.  erff: 55, and nothing left of the value below g = -5.)
 __device__ __forceinline__ float normal_cdf(float g, float e) {
     const float t = rcp(fmaf(fabsf(g), 0.31f, 1.f));
     float c = fmaf(t, -0.0739276037f, 0.1804459095f);
