@@ -285,7 +285,9 @@ KRON_API kron_status_t kron_vanloan_fit(const void *W, int p, int q, int m1, int
  * (workspace may then be NULL), but for some shapes and many rows in KRON_F32.  0 also means
  * arguments that the call refuses, and for the backward with N > 0 only that; whether the forward
  * has a kernel for a shape, a call with N = 0 tells without launching anything.  A backward that is
- * refused does not keep the forward from running.  N <= 2^30.
+ * refused does not keep the forward from running.  For the KRON_BF16 backward of more than eight
+ * rows it holds x^T dg and x^T du in float32 (8 p m1 q m2 bytes, and as much again for each range
+ * that many rows are split into) beside dg and du.  N <= 2^30.
  * Results are bitwise reproducible on one GPU model.  Everything else as for the layer.
  */
 typedef enum {

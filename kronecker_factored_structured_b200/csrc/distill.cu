@@ -15,8 +15,8 @@
 // differences from a value next to the row's maximum, however far from zero the logits are.
 // Bound: HBM moves the logits once in and once out (126 us for 4096 x 50257 bf16); per element
 // and pass one ex2 (two for a tau other than 1, 2 and 4), 92 us on the special-function units,
-// and with the packed FP32 instructions some 11 issue slots.  Measured FIGSTEP (an earlier form
-// with six CTAs per SM 181; with scalar FP32 instructions 191; 512 threads, three CTAs per SM:
+// and with the packed FP32 instructions some 11 issue slots.  Measured 184 to 188 us
+// (earlier forms of it: 181; with scalar FP32 instructions 191; 512 threads, three CTAs per SM:
 // 212; rows split over clusters of four CTAs and held in registers, one read: 301, the barriers
 // of the shorter pieces not covered).  740 rows at work exceed L2 where a row has more than 170
 // KB: 1024 x 50257 fp32 read 333 MB for 206, 1024 x 131072 bf16 462 for 268.
@@ -682,7 +682,7 @@ kron_status_t bad(kron_status_t st, const char *fmt, double a = 0, double b = 0)
 }
 
 // Threads per row: with more than four rows per SM 256, with fewer as many as let all rows run at
-// once (515 x 50257 fp32 with its gradient: 58 us with 256 threads, 52 with 384).
+// once (515 x 50257 fp32 with its gradient: 58 us with 256 threads, 53 with 384).
 template <typename T, int E, bool STATS, bool GRAD>
 cudaError_t launch(int64_t N, const Args &g, cudaStream_t st) {
     if (g.V <= kShortV && g.K <= kShortK)

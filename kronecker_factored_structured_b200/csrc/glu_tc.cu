@@ -23,10 +23,16 @@
 // set-up of the factors is what takes the time.  Stage 1 is repeated for each c slice.
 // Bound by the SM's shared-memory pipe and issue slots: per chunk 32 KB of T are stored and read
 // back beside the MMAs' other operands, 512 cycles at 128 B/clk for the 32 x 32 blocks against
-// 256 cycles of MMA.  20000 x 1024, r = 4: 44 us, 74% of the pipe's cycles (36 the warps', 38 the
-// tensor core's), 75% of the issue slots, 0.95 TB/s of HBM; 16384 x 4096, r = 8: 390 us, 705
-// TFLOP/s.  Backward of the 20000 rows: pre-activations' gradients 66 us (epilogue 2's latency:
-// three reads and two stores per element), dX 43.
+// 256 cycles of MMA.  20000 x 1024, r = 4: 45 us, 73% of the pipe's cycles (35 the warps', 38 the
+// tensor core's), 74% of the issue slots, 0.91 TB/s of HBM.  Backward of these rows:
+// pre-activations' gradients 67 us (epilogue 2's latency: three reads and two stores per element),
+// dX 44.
+// Wide layers whose factors of both projections exceed one SM's shared memory (64 x 64 blocks, r =
+// 8: 262 KB) are bound by repeats instead: two slices of c, so that every T is formed, stored and
+// read back twice, and stage-2 MMAs of N = 32, which take 74 cycles where 16 is the rate.  16384 x
+// 4096, r = 8: 391 us, 703 TFLOP/s, from a cool GPU and 450 us, 611 TFLOP/s, under the power cap;
+// two forward calls of the layer (176 us each) and an elementwise gate (62 us of HBM traffic) take
+// as long.
 #include "glu.h"
 #include "tc_gen_common.cuh"
 

@@ -4,13 +4,16 @@
 //   dC_i[a,c] = sum_(j,k) B_i[j,k] dW[a,j,c,k]     dA_i = dC_i (.) S, dS = sum_i dC_i (.) A_i
 //   dB_i[j,k] = sum_(a,c) C_i[a,c] dW[a,j,c,k]     dbias = column sums of d
 // dW is formed densely by one tcgen05 product over the rows (both operands as they lie in
-// memory, MN-major), then contracted with the factors in fp32.  For the vec trick's own order
-// (T = X B against d, C d against X) the row sums take r (1/q + 1/m1) of dW's multiply-adds,
-// twice, but T and C d of every row have to go through registers and shared memory, which is
-// what bounds those kernels; dW is a plain product that runs at the tensor cores' rate.
+// memory, MN-major), then contracted with the factors in fp32.  The vec trick's own order (T = X B
+// against d, C d against X) takes 2 r (1/q + 1/m1) of dW's multiply-adds, and T and C d of every
+// row through registers and shared memory; dW is a plain product at the tensor cores' rate.  That
+// ratio is 1/2 for 1024 x 1024, 32 x 32 blocks and r = 4, but 1/16 for 4096 x 4096, 64 x 64 blocks
+// and r = 1: wide layers of low rank pay for dW, as no kernel here takes the other order above
+// eight rows (backward of 16384 rows of 4096: 1135 us for r = 1, 2017 for r = 8).  The workspace
+// holds dW of both projections in fp32 (134 MB at 4096 x 4096).
 // Rows are split into ranges whose dW are added in order: bitwise reproducible.
-// 20000 rows, 1024 x 1024: dW 70 us, 1.2 PFLOP/s on 128 of the 148 SMs (76% of the tensor pipe's
-// cycles on them), the contraction 17 us, a read of 34 MB from L2 and HBM.  1021 rows, 768 x 2048:
+// 20000 rows, 1024 x 1024: dW 72 us, 1.2 PFLOP/s on 128 of the 148 SMs (76% of the tensor pipe's
+// cycles on them), the contraction 19 us, a read of 34 MB from L2 and HBM.  1021 rows, 768 x 2048:
 // 20 and 18 us, both short of work for the SMs: 16 steps of 64 rows, and the latency of its loads.
 #include "glu.h"
 #include "tc_gen_common.cuh"

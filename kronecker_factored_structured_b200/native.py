@@ -585,7 +585,8 @@ def distill_backward(logits, values, indices, lse, dloss=None, labels=None, weig
 def distill_step(logits, values, indices, labels=None, weights=None, temperature=1.0,
                  label_weight=0.0, out=None, stream=None):
     """Loss of each row and the gradient of their sum in one call: dict(loss [N], dlogits).
-    ``out`` may be the logits themselves."""
+    ``out`` may be the logits themselves.  Where the logits' rows lie further apart than their
+    length, an ``out`` of the same stride is stored fastest."""
     N, V, K, head, dtype, dev = _distill_args(logits, values, indices, labels, weights,
                                               label_weight)
     with _on_device(dev, stream):
