@@ -6,7 +6,7 @@
 //   loss = w [ (1 - lam) tau^2 sum_j p_j (log p_j - log q_{i_j}) + lam (lse(x) - x_label) ]
 //   dx_v = w dl [ (1 - lam) tau (q_v - sum_{j: i_j = v} p_j) + lam (softmax(x)_v - [v = label]) ]
 //
-// One CTA of 256 threads per row, five or six per SM (more threads where there are few rows).
+// One CTA of 256 threads per row, five to eight per SM (more threads where there are few rows).
 // Pass 1 reads the row with a running maximum m per thread and the sums of exp((x - m)/tau) and
 // exp(x - m); pass 2 (gradient) reads it again, from L2 where the rows at work fit there, and
 // writes the dense part c_t q + c_1 softmax(x); the K + 1 columns that the teacher and the label
